@@ -91,8 +91,16 @@ enum qkq_status_bits {
     QKQ_STATUS_TIMEOUT = 8,        /* a bounded on-chip wait gave up; outputs incomplete   */
     QKQ_STATUS_EMPTY_STREAM = 16,  /* qkq_solve_angles: a stream the estimator uses had no
                                       observations; those pairs got phi = 0               */
-    QKQ_STATUS_BOUNDS = 32         /* bounds-checking debug build only: an index check of a
+    QKQ_STATUS_BOUNDS = 32,        /* bounds-checking debug build only: an index check of a
                                       copy or store failed; that access was skipped        */
+    QKQ_STATUS_CACHE_INDEX = 128   /* paged cache: a page id, length or row range was outside
+                                      its buffer; that page or sequence was left out       */
+};
+
+/* 16-bit type of the q, k, v and output tensors of the paged 8-bit cache's calls. */
+enum qkq_dtype {
+    QKQ_DTYPE_BF16 = 0,
+    QKQ_DTYPE_FP16 = 1
 };
 
 /* Library version (major * 10000 + minor * 100 + patch). */
@@ -352,6 +360,106 @@ int qkq_attention_scores_tc(const void *q_bf16, int64_t Tq, const uint8_t *k_cod
 int qkq_attention_scores_mma(const void *q_bf16, int64_t Tq, const uint8_t *k_codes,
                              const void *k_scales_f16, int64_t Tk, int Hq, int Hkv, int d_h,
                              int group, float *scores, qkq_stream_t stream);
+
+/*
+ * The paged 8-bit key/value cache (KV8): qkq_append_kv8 writes it, qkq_attention_kv8 reads it.
+ *   Where the int4 cache above keeps one contiguous sequence's rotated keys and gives their
+ *   logits, this one keeps keys and values of many sequences in pages and gives the attention's
+ *   output.  It serves keys as RoPE leaves them: e4m3 codes keep a relative precision, so loud
+ *   channels need no rotation first.
+ *   codes  [num_pages][Hkv][page_size][d_h] e4m3 (uint8), keys and values in one buffer each;
+ *   steps  [num_pages][Hkv] fp32, one per page (block of page_size tokens) and key head, for
+ *          keys and for values: a cached value is step * code.  qkq_append_kv8 writes powers of
+ *          two in [2^-40, 2^40]; qkq_attention_kv8 reads any finite value, those outside that
+ *          range (and NaN) as its nearest end.
+ *   block_table [B][max_pages] int32: the page id of each of a sequence's blocks, in order.
+ *   seq_lens [B] int32: cached tokens of each sequence, this step's new ones included (they are
+ *          its last ones), in both calls.
+ *   cu_new [B + 1] int32, nullable: sequence b's new tokens are rows cu_new[b] .. cu_new[b + 1]
+ *          - 1 of the batch's T rows, cu_new[0] = 0.  Rows from cu_new[B] on belong to no sequence:
+ *          outputs there are left as they were.  NULL: one new token per sequence (T == B).
+ *   The index tensors live on the device and are checked there: a page id outside
+ *   [0, num_pages), a length above max_pages * page_size or a row range outside [0, T) sets
+ *   QKQ_STATUS_CACHE_INDEX and that page or sequence is left out; nothing outside the buffers is
+ *   read or written.
+ *   Supported: d_h in {64, 128}, page_size in {16, 32, 64, 128}, bf16 or fp16 tensors, any
+ *   Hq that is a multiple of Hkv.  16-byte aligned q, k, v, q_out, out, codes, tables, workspace.
+ */
+
+/*
+ * qkq_append_kv8 — new keys and values into their pages, RoPE on the way; queries rotated in the
+ *   same launch.
+ *   RoPE turns the pairs of the first rot_dim channels (half layout: channel k with
+ *   k + rot_dim/2; interleaved: 2k with 2k + 1) with the table row of the token's position, in
+ *   the fp32 sequence of qkq_transform_quantize; channels from rot_dim on pass.  Scaled
+ *   positions come in through the table (inv_freq_host of qkq_rope_table, or any fp32 table).
+ *   Per page and key head: step = the smallest power of two with max|y| <= 448 step over the
+ *   page's new tokens, within [2^-40, 2^40], and at least the page's present step where it
+ *   held tokens of the sequence already; code = e4m3(y / step), rounded once to nearest even,
+ *   saturating.  Where a partly full page's step grows, the codes it holds are rounded again to the
+ *   new step (exact but for values that fall under e4m3's smallest normal number).  A page's first
+ *   token starts it afresh.  Rows of a page behind the sequence's last token are left as they were.
+ *   Non-finite inputs set QKQ_STATUS_NONFINITE and do not count for the step: infinities saturate,
+ *   NaN becomes the code 0x7f.  max|y| > 448 * 2^40 sets QKQ_STATUS_SCALE_OVERFLOW.
+ * Arguments
+ *   q [T][Hq][d_h] (nullable with q_out: no queries), k, v [T][Hkv][d_h]: device; rows of a token
+ *     contiguous, q_stride / k_stride / v_stride elements from token to token (a multiple of 8;
+ *     a fused projection's output can be passed as it is).
+ *   dtype: qkq_dtype.  pos [T] int32, nullable: RoPE positions; NULL takes each token's index in its
+ *     sequence.  Positions outside [0, max_pos) are clamped and set QKQ_STATUS_POS_RANGE.
+ *   rot_dim: a multiple of 16 in [0, d_h]; 0: no rotation (tables may be NULL).
+ *   rope_style: QKQ_ROPE_HALF or QKQ_ROPE_INTERLEAVED (split tables: QKQ_ERR_UNSUPPORTED).
+ *   cos_tab / sin_tab [max_pos][rot_dim/2] fp32.
+ *   q_out [T][Hq][d_h]: rotated queries, contiguous; may be q itself when that is contiguous, must
+ *     not overlap q, k or v otherwise.
+ *   k_codes, v_codes, k_steps, v_steps: the cache, updated in place.  A page that receives tokens
+ *     must not be one that another sequence of the call uses (pages of a shared prefix may be in
+ *     several block tables as long as they are full).
+ * Returns QKQ_OK (T == 0 or B == 0: nothing), or a negative qkq_err (nothing launched).
+ */
+int qkq_append_kv8(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, int dtype, const int32_t *pos, int64_t T,
+                   const int32_t *cu_new, const int32_t *seq_lens, int B,
+                   const int32_t *block_table, int max_pages, int64_t num_pages, int page_size,
+                   int Hq, int Hkv, int d_h, int rot_dim, int rope_style, const float *cos_tab,
+                   const float *sin_tab, int max_pos, void *q_out, uint8_t *k_codes,
+                   uint8_t *v_codes, float *k_steps, float *v_steps, int *status,
+                   qkq_stream_t stream);
+
+/*
+ * qkq_attention_kv8_workspace_bytes — scratch needed by qkq_attention_kv8 for these sizes (partial
+ *   rows of the work split; 0 when T == 0 or B == 0).
+ */
+size_t qkq_attention_kv8_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int d_h);
+
+/*
+ * qkq_attention_kv8 — causal attention of new tokens over the paged 8-bit cache.
+ *   Token t of sequence b stands at index i = seq_lens[b] - n_b + t (n_b its new tokens) and sees
+ *   cached token j when j <= i, and with window > 0 also j > i - window or j < sinks (a few first
+ *   tokens that stay visible):
+ *     out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j][h / (Hq/Hkv)]) V[j][h / (Hq/Hkv)].
+ *   A row that sees nothing (i < 0) gets zeros and a log-sum-exp of -inf.
+ *   Products of the queries (scaled per row by a power of two into fp16) and the codes, fp32 sums,
+ *   softmax statistics and outputs in fp32, probabilities rounded to fp16 before their product with
+ *   the values, the output rounded once to dtype.  A cached NaN code reaches exactly the rows that
+ *   see it; what lies in pages behind a sequence's length, or in masked places, reaches none.
+ *   Deterministic for a device and the sizes and lengths.
+ * Arguments
+ *   q [T][Hq][d_h] (device, dtype).  scale: finite (usually 1/sqrt(d_h)).  window >= 0 (0: none),
+ *   sinks >= 0 (used with a window).
+ *   out [T][Hq][d_h] dtype (device, written; may be q).  lse [T][Hq] fp32, nullable: natural log of
+ *     the softmax's denominator.
+ *   workspace: at least qkq_attention_kv8_workspace_bytes(...) bytes, contents irrelevant; calls
+ *     that may overlap on the GPU need one each.
+ *   status: nullable, QKQ_STATUS_CACHE_INDEX (QKQ_STATUS_TIMEOUT: a bounded on-chip wait gave up).
+ * Returns QKQ_OK (T == 0 or B == 0: nothing), or a negative qkq_err (nothing launched).
+ */
+int qkq_attention_kv8(const void *q, int dtype, int64_t T, const int32_t *cu_new,
+                      const int32_t *seq_lens, int B, const int32_t *block_table, int max_pages,
+                      int64_t num_pages, int page_size, const uint8_t *k_codes,
+                      const uint8_t *v_codes, const float *k_steps, const float *v_steps, int Hq,
+                      int Hkv, int d_h, float scale, int window, int sinks, void *out, float *lse,
+                      void *workspace, size_t workspace_bytes, int *status, qkq_stream_t stream);
 
 /*
  * qkq_accumulate_moments — calibration side path, step 1.

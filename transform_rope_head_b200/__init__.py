@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 __all__ = [
     "MODES", "ESTIMATORS", "ROPE_STYLES", "STATUS_BITS", "QKQError", "lib", "lib_path",
@@ -22,6 +23,7 @@ __all__ = [
     "transform_quantize_tc", "transform_quantize_qkv", "transform_quantize_stats",
     "transform_quantize_calibrate",
     "attention_scores",
+    "KV8Cache", "kv8_cache", "append_kv8", "attention_kv8", "attention_kv8_workspace_bytes",
     "accumulate_moments", "accumulate_moments_noalloc",
     "solve_angles",
     "dequant_error", "dequant_error_recompute", "dequant_summary", "moments_workspace_bytes",
@@ -34,7 +36,7 @@ ESTIMATORS = {"pooled": 0, "k_only": 1, "balanced": 2}
 ROPE_STYLES = {"half": 0, "interleaved": 1}
 ROPE_SPLIT_TABLE = 0x100  # flag OR-ed into the style: split (two-level) RoPE tables
 STATUS_BITS = {"nonfinite": 1, "scale_overflow": 2, "pos_range": 4, "timeout": 8,
-               "empty_stream": 16, "bounds": 32}
+               "empty_stream": 16, "bounds": 32, "cache_index": 128}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # QKQ_LIB_PATH selects another build of the library (e.g. a tuning variant)
@@ -47,7 +49,8 @@ SYMBOLS = ("qkq_version", "qkq_error_string", "qkq_status_string", "qkq_rope_tab
            "qkq_moments_workspace_bytes", "qkq_accumulate_moments",
            "qkq_solve_angles", "qkq_dequant_error_workspace_bytes", "qkq_dequant_error",
            "qkq_dequant_error_recompute", "qkq_dequant_summary",
-           "qkq_accumulate_moments_noalloc")
+           "qkq_accumulate_moments_noalloc",
+           "qkq_append_kv8", "qkq_attention_kv8_workspace_bytes", "qkq_attention_kv8")
 
 
 class QKQError(RuntimeError):
@@ -109,6 +112,14 @@ def _load() -> ctypes.CDLL:
     L.qkq_dequant_error_recompute.argtypes = [P, P, I64, I, I, I, P, P, I, P, I, I, I, P, P, P,
                                               P, SZ, P, P]
     L.qkq_dequant_error_recompute.restype = I
+    L.qkq_append_kv8.argtypes = [P, I64, P, I64, P, I64, I, P, I64, P, P, I, P, I, I64, I, I, I, I,
+                                 I, I, P, P, I, P, P, P, P, P, P, P]
+    L.qkq_append_kv8.restype = I
+    L.qkq_attention_kv8_workspace_bytes.argtypes = [I64, I, I, I, I]
+    L.qkq_attention_kv8_workspace_bytes.restype = SZ
+    L.qkq_attention_kv8.argtypes = [P, I, I64, P, P, I, P, I, I64, I, P, P, P, P, I, I, I,
+                                    ctypes.c_float, I, I, P, P, P, SZ, P, P]
+    L.qkq_attention_kv8.restype = I
     L.qkq_dequant_summary.argtypes = [P, P]
     L.qkq_dequant_summary.restype = I
     return L
@@ -395,6 +406,203 @@ def attention_scores_mma(q_t, k_codes, k_scales, *, scores=None, stream=None):
                                          hkv, d_h, group, _ptr(scores), _stream(stream)),
            "qkq_attention_scores_mma")
     return scores
+
+
+# ---------------------------------------------------------------- paged KV8 cache -
+
+class KV8Cache(NamedTuple):
+    """A paged 8-bit key/value cache: e4m3 codes [num_pages, Hkv, page_size, d_h]
+    (torch.float8_e4m3fn) and one fp32 step per page and key head [num_pages, Hkv], for keys
+    and for values; a cached number is step * code."""
+    k: "torch.Tensor"
+    v: "torch.Tensor"
+    k_steps: "torch.Tensor"
+    v_steps: "torch.Tensor"
+
+
+def kv8_cache(num_pages: int, Hkv: int, page_size: int, d_h: int, device="cuda") -> KV8Cache:
+    """An empty KV8Cache (zero codes)."""
+    import torch
+    k, v = (torch.zeros((num_pages, Hkv, page_size, d_h), dtype=torch.uint8,
+                        device=device).view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.full((num_pages, Hkv), 2.0 ** -40, dtype=torch.float32, device=device)
+              for _ in range(2))
+    return KV8Cache(k, v, ks, vs)
+
+
+def _kv8_dtype(t, name):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return 0
+    if t.dtype is torch.float16:
+        return 1
+    raise ValueError(f"{name} must be bfloat16 or float16")
+
+
+def _kv8_index(dev, T, cache, block_table, seq_lens, cu_new):
+    """Checks of the cache and the index tensors; (B, max_pages, num_pages, Hkv, page_size, d_h)."""
+    import torch
+    k, v, ks, vs = cache
+    num_pages, Hkv, ps, d_h = k.shape
+    if k.dtype is not torch.float8_e4m3fn or v.dtype is not torch.float8_e4m3fn:
+        raise ValueError("cache codes must be float8_e4m3fn")
+    if ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
+        raise ValueError("cache steps must be float32")
+    if v.shape != k.shape or tuple(ks.shape) != (num_pages, Hkv) or vs.shape != ks.shape:
+        raise ValueError("cache shapes differ: codes [pages, Hkv, page_size, d_h], steps [pages, Hkv]")
+    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    B, max_pages = block_table.shape
+    index = [block_table, seq_lens]
+    if cu_new is not None:
+        if tuple(cu_new.shape) != (B + 1,):
+            raise ValueError("cu_new must be [B + 1]")
+        index.append(cu_new)
+    elif T != B:
+        raise ValueError("without cu_new there is one new token per sequence")
+    for t in index:
+        if t.dtype is not torch.int32:
+            raise ValueError("block_table, seq_lens and cu_new must be int32")
+    for t in (k, v, ks, vs, *index):
+        if not t.is_contiguous():
+            raise ValueError("the cache and the index tensors must be contiguous")
+        if t.device != dev:
+            raise ValueError("all tensors must be on one CUDA device")
+    return B, max_pages, num_pages, Hkv, ps, d_h
+
+
+def _kv8_rows(t, name, T, H, d_h, dtype, dev):
+    """Elements from token to token of [T, H, d_h] rows (each token's heads contiguous)."""
+    if tuple(t.shape) != (T, H, d_h) or t.dtype is not dtype or t.device != dev:
+        raise ValueError(f"{name} must be [T, heads, d_h] of one type and device with the others")
+    st, sh, sd = t.stride()
+    if (sd != 1 or sh != d_h) and t.numel():
+        if not (H == 1 and sd == 1):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st if T > 1 else max(st, H * d_h) // 8 * 8
+
+
+class _OnDevice:
+    """The tensors' device as the current one for a call (a no-op when it is), and its stream; new
+    tensors used on another stream than the allocating one are recorded on it."""
+
+    def __init__(self, dev, stream):
+        import torch
+        if dev.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        here = torch.cuda.current_stream(dev)
+        self.stream = here if stream is None else stream
+        self.other = self.stream if self.stream != here else None
+        self.guard = torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else None
+
+    def new(self, t):
+        if self.other is not None:
+            t.record_stream(self.other)
+        return t
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def append_kv8(k, v, cache, block_table, seq_lens, cu_new=None, *, q=None, pos=None, cos_tab=None,
+               sin_tab=None, rope_style="half", q_out=None, status=None, stream=None):
+    """Append new keys and values k, v [T, Hkv, d_h] (bf16 or fp16) to their sequences' pages of
+    ``cache`` (a KV8Cache, updated in place), RoPE applied to the keys on the way, and rotate the
+    queries q [T, Hq, d_h] in the same launch (``qkq_append_kv8``).
+
+    seq_lens [B] int32 counts each sequence's cached tokens, the new ones included; block_table
+    [B, max_pages] int32 lists its pages; cu_new [B + 1] int32 its rows of the batch (None: one new
+    token per sequence).  cos_tab / sin_tab [max_pos, rot_dim/2] fp32 rotate the first rot_dim
+    channels (None: no rotation) at pos [T] int32 (None: each token's index in its sequence).
+    k, v and q may be parts of one fused [T, heads, d_h] tensor.  Returns q_out (None without q)."""
+    import torch
+    dev = k.device
+    T, _, d_h = k.shape
+    dtype = _kv8_dtype(k, "k")
+    B, max_pages, num_pages, Hkv, ps, dc = _kv8_index(dev, T, cache, block_table, seq_lens, cu_new)
+    ks = _kv8_rows(k, "k", T, Hkv, dc, k.dtype, dev)
+    vs = _kv8_rows(v, "v", T, Hkv, dc, k.dtype, dev)
+    on = _OnDevice(dev, stream)
+    Hq, qs = Hkv, 0
+    if q is not None:
+        Hq = q.shape[1]
+        qs = _kv8_rows(q, "q", T, Hq, dc, k.dtype, dev)
+        if q_out is None:
+            q_out = on.new(torch.empty((T, Hq, dc), dtype=q.dtype, device=dev))
+        elif q_out.shape != q.shape or q_out.dtype is not q.dtype or not q_out.is_contiguous() \
+                or q_out.device != dev:
+            raise ValueError("q_out must be a contiguous tensor like q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = max_pos = 0
+    if (cos_tab is None) != (sin_tab is None):
+        raise ValueError("cos_tab and sin_tab go together")
+    if cos_tab is not None:
+        max_pos, rot = cos_tab.shape
+        rot *= 2
+        for t in (cos_tab, sin_tab):
+            if t.dtype is not torch.float32 or not t.is_contiguous() or t.device != dev \
+                    or t.shape != cos_tab.shape:
+                raise ValueError("cos_tab and sin_tab must be contiguous float32 [max_pos, rot_dim/2]")
+    if pos is not None and (pos.dtype is not torch.int32 or tuple(pos.shape) != (T,)
+                            or not pos.is_contiguous() or pos.device != dev):
+        raise ValueError("pos must be int32 [T]")
+    with on as s:
+        _check(_lib.qkq_append_kv8(
+            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, dtype, _ptr(pos), T, _ptr(cu_new), _ptr(seq_lens),
+            B, _ptr(block_table), max_pages, num_pages, ps, Hq, Hkv, dc, rot, ROPE_STYLES[rope_style],
+            _ptr(cos_tab), _ptr(sin_tab), max_pos, _ptr(q_out), _ptr(cache.k), _ptr(cache.v),
+            _ptr(cache.k_steps), _ptr(cache.v_steps), _ptr(status), s), "qkq_append_kv8")
+    return q_out
+
+
+def attention_kv8_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, d_h: int) -> int:
+    return int(_lib.qkq_attention_kv8_workspace_bytes(int(T), int(B), int(Hq), int(Hkv), int(d_h)))
+
+
+def attention_kv8(q, cache, block_table, seq_lens, cu_new=None, *, scale=None, window=0, sinks=0,
+                  out=None, lse=None, want_lse=False, workspace=None, status=None, stream=None):
+    """Causal attention of new tokens' queries q [T, Hq, d_h] (bf16 or fp16, rotated) over the
+    paged 8-bit ``cache`` (``qkq_attention_kv8``); index tensors as in append_kv8, which has
+    written these tokens' keys and values.  window > 0 limits a token to its last ``window``
+    cached tokens and the first ``sinks``.  scale: 1/sqrt(d_h) when None.  Returns out, or
+    (out, lse) with want_lse or a given lse [T, Hq] fp32."""
+    import torch
+    dev = q.device
+    T, Hq, d_h = q.shape
+    dtype = _kv8_dtype(q, "q")
+    B, max_pages, num_pages, Hkv, ps, dc = _kv8_index(dev, T, cache, block_table, seq_lens, cu_new)
+    if dc != d_h or not q.is_contiguous():
+        raise ValueError("q must be contiguous [T, Hq, d_h] with the cache's d_h")
+    on = _OnDevice(dev, stream)
+    if out is None:
+        out = on.new(torch.empty_like(q))
+    elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous tensor like q")
+    if lse is None and want_lse:
+        lse = on.new(torch.empty((T, Hq), dtype=torch.float32, device=dev))
+    elif lse is not None and (tuple(lse.shape) != (T, Hq) or lse.dtype is not torch.float32
+                              or not lse.is_contiguous() or lse.device != dev):
+        raise ValueError("lse must be contiguous float32 [T, Hq]")
+    if workspace is None:
+        need = attention_kv8_workspace_bytes(T, B, Hq, Hkv, d_h)
+        workspace = on.new(torch.empty(need, dtype=torch.uint8, device=dev)) if need else None
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous on the tensors' device")
+    with on as s:
+        _check(_lib.qkq_attention_kv8(
+            _ptr(q), dtype, T, _ptr(cu_new), _ptr(seq_lens), B, _ptr(block_table), max_pages, num_pages,
+            ps, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_steps), _ptr(cache.v_steps), Hq, Hkv, d_h,
+            float(d_h ** -0.5 if scale is None else scale), int(window), int(sinks), _ptr(out), _ptr(lse),
+            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+            _ptr(status), s), "qkq_attention_kv8")
+    return out if lse is None else (out, lse)
 
 
 # ---------------------------------------------------------------- calibration -----

@@ -127,6 +127,31 @@ size_t dequant_ws(int64_t T, int Hkv)
     return static_cast<size_t>(qkq::dequant_max_ctas(T)) * 6 * sizeof(double);
 }
 
+// Sizes and index tensors of the paged 8-bit cache's calls.
+int kv8_index(int64_t T, const int32_t *cu_new, const int32_t *seq_lens, int B, const int32_t *block_table,
+              int max_pages, int64_t num_pages, int page_size, int Hq, int Hkv, int d_h, int dtype, qkq::KV8Index *x)
+{
+    if (dtype != QKQ_DTYPE_BF16 && dtype != QKQ_DTYPE_FP16) return QKQ_ERR_ARG;
+    if (T < 0 || T > INT32_MAX || B < 0 || (d_h != 64 && d_h != 128)) return QKQ_ERR_SHAPE;
+    if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Hq > 65536) return QKQ_ERR_SHAPE;
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return QKQ_ERR_SHAPE;
+    if (max_pages < 1 || num_pages < 1 || num_pages > INT32_MAX) return QKQ_ERR_SHAPE;
+    if (!cu_new && T != B) return QKQ_ERR_SHAPE;
+    if (T * (Hq / Hkv) > INT32_MAX) return QKQ_ERR_SHAPE;  // 32-bit query row indices
+    if (T == 0 || B == 0) return QKQ_OK;
+    if (!seq_lens || !block_table) return QKQ_ERR_ARG;
+    if (!aligned(cu_new, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4)) return QKQ_ERR_ALIGN;
+    x->T = T;
+    x->cu = cu_new;
+    x->seq_lens = seq_lens;
+    x->block_table = block_table;
+    x->B = B;
+    x->max_pages = max_pages;
+    x->num_pages = num_pages;
+    x->page_shift = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    return QKQ_OK;
+}
+
 // qkq_transform_quantize and its Q/K/V form (v_bf16 == nullptr: no value rows).
 int transform_call(const void *q_bf16, const void *k_bf16, const void *v_bf16, const int32_t *pos,
                    int64_t T, int Hq, int Hkv, int d_h, int rope_style, const float *cos_tab,
@@ -230,23 +255,25 @@ const char *qkq_error_string(int code)
 
 const char *qkq_status_string(int s)
 {
-    static const char *bit_names[6] = {"nonfinite", "scale_overflow", "pos_range", "timeout",
-                                       "empty_stream", "bounds"};
-    static char names[64][96];  // every combination of the six bits, built once
+    static const char *bit_names[7] = {"nonfinite", "scale_overflow", "pos_range", "timeout",
+                                       "empty_stream", "bounds", "cache_index"};
+    static char names[128][96];  // every combination of the seven bits, built once
     static std::once_flag once;
     std::call_once(once, [] {
-        for (int v = 0; v < 64; ++v) {
+        for (int v = 0; v < 128; ++v) {
             char *out = names[v];
             out[0] = 0;
             if (v == 0) strcpy(out, "ok");
-            for (int b = 0; b < 6; ++b)
+            for (int b = 0; b < 7; ++b)
                 if (v & (1 << b)) {
                     if (out[0]) strcat(out, "|");
                     strcat(out, bit_names[b]);
                 }
         }
     });
-    return (s >= 0 && s < 64) ? names[s] : "unknown status bits";
+    // bit 6 is not assigned, bit 7 is the seventh name
+    const bool known = s >= 0 && s < 256 && (s & 64) == 0;
+    return known ? names[(s & 63) | (s & QKQ_STATUS_CACHE_INDEX) >> 1] : "unknown status bits";
 }
 
 int qkq_rope_table(float *cos_host, float *sin_host, int max_pos, int d_h, double theta,
@@ -548,6 +575,120 @@ int qkq_attention_scores_mma(const void *q_bf16, int64_t Tq, const uint8_t *k_co
     if (rc) return rc < 0 ? rc : QKQ_OK;
     if (Tk * Hkv > 0xffffffffll) return QKQ_ERR_SHAPE;  // 32-bit cache row indices
     return from_cuda(qkq::attention_scores_mma_launch(p, dev, d_h, group, stream));
+}
+
+int qkq_append_kv8(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, int dtype, const int32_t *pos, int64_t T,
+                   const int32_t *cu_new, const int32_t *seq_lens, int B,
+                   const int32_t *block_table, int max_pages, int64_t num_pages, int page_size,
+                   int Hq, int Hkv, int d_h, int rot_dim, int rope_style, const float *cos_tab,
+                   const float *sin_tab, int max_pos, void *q_out, uint8_t *k_codes,
+                   uint8_t *v_codes, float *k_steps, float *v_steps, int *status,
+                   qkq_stream_t stream)
+{
+    const NvtxRange nvtx_range("qkq_append_kv8");
+    qkq::AppendKV8Params p{};
+    int rc = kv8_index(T, cu_new, seq_lens, B, block_table, max_pages, num_pages, page_size, Hq, Hkv, d_h, dtype, &p.x);
+    if (rc) return rc;
+    const int pairs = rope_style & ~QKQ_ROPE_SPLIT_TABLE;
+    if (pairs != QKQ_ROPE_HALF && pairs != QKQ_ROPE_INTERLEAVED) return QKQ_ERR_ARG;
+    if (split_table(rope_style)) return QKQ_ERR_UNSUPPORTED;
+    if (rot_dim < 0 || rot_dim > d_h || rot_dim % 16 != 0) return QKQ_ERR_SHAPE;
+    if (rot_dim > 0 && max_pos < 1) return QKQ_ERR_SHAPE;
+    if (T == 0 || B == 0) return QKQ_OK;
+    if (!k || !v || !k_codes || !v_codes || !k_steps || !v_steps) return QKQ_ERR_ARG;
+    if ((q == nullptr) != (q_out == nullptr)) return QKQ_ERR_ARG;
+    if (rot_dim > 0 && (!cos_tab || !sin_tab)) return QKQ_ERR_ARG;
+    const int64_t rq = static_cast<int64_t>(Hq) * d_h, rk = static_cast<int64_t>(Hkv) * d_h;
+    if ((q && (q_stride < rq || q_stride % 8)) || k_stride < rk || k_stride % 8 || v_stride < rk || v_stride % 8)
+        return QKQ_ERR_SHAPE;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_codes, 16) ||
+        !aligned(v_codes, 16) || !aligned(cos_tab, 16) || !aligned(sin_tab, 16) || !aligned(k_steps, 4) ||
+        !aligned(v_steps, 4) || !aligned(pos, 4) || !aligned(status, 4))
+        return QKQ_ERR_ALIGN;
+    if (q) {
+        const size_t out = static_cast<size_t>(T) * rq * 2;
+        auto span = [&](int64_t stride, int64_t row) { return (static_cast<size_t>(T - 1) * stride + row) * 2; };
+        const bool in_place = q == q_out && q_stride == rq;
+        if ((!in_place && overlaps(q, span(q_stride, rq), q_out, out)) || overlaps(k, span(k_stride, rk), q_out, out) ||
+            overlaps(v, span(v_stride, rk), q_out, out))
+            return QKQ_ERR_ARG;
+    }
+    const size_t pool = static_cast<size_t>(num_pages) * rk * page_size;
+    if (overlaps(k_codes, pool, v_codes, pool)) return QKQ_ERR_ARG;
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.half = dtype == QKQ_DTYPE_FP16;
+    p.pos = pos;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.rot = rot_dim;
+    p.interleaved = pairs == QKQ_ROPE_INTERLEAVED;
+    p.cos_t = cos_tab;
+    p.sin_t = sin_tab;
+    p.max_pos = max_pos;
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.k_codes = k_codes;
+    p.v_codes = v_codes;
+    p.k_steps = k_steps;
+    p.v_steps = v_steps;
+    p.status = status;
+    return from_cuda(qkq::append_kv8_launch(p, d_h, stream));
+}
+
+size_t qkq_attention_kv8_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int d_h)
+{
+    if (T <= 0 || B <= 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || (d_h != 64 && d_h != 128)) return 0;
+    return qkq::attention_kv8_workspace(T, B, Hq, Hkv, d_h);
+}
+
+int qkq_attention_kv8(const void *q, int dtype, int64_t T, const int32_t *cu_new,
+                      const int32_t *seq_lens, int B, const int32_t *block_table, int max_pages,
+                      int64_t num_pages, int page_size, const uint8_t *k_codes,
+                      const uint8_t *v_codes, const float *k_steps, const float *v_steps, int Hq,
+                      int Hkv, int d_h, float scale, int window, int sinks, void *out, float *lse,
+                      void *workspace, size_t workspace_bytes, int *status, qkq_stream_t stream)
+{
+    const NvtxRange nvtx_range("qkq_attention_kv8");
+    qkq::AttnKV8Params p{};
+    int rc = kv8_index(T, cu_new, seq_lens, B, block_table, max_pages, num_pages, page_size, Hq, Hkv, d_h, dtype, &p.x);
+    if (rc) return rc;
+    if (!isfinite(scale) || window < 0 || sinks < 0) return QKQ_ERR_ARG;
+    if (T == 0 || B == 0) return QKQ_OK;
+    if (!q || !out || !k_codes || !v_codes || !k_steps || !v_steps) return QKQ_ERR_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_steps, 4) ||
+        !aligned(v_steps, 4) || !aligned(lse, 4) || !aligned(workspace, 16) || !aligned(status, 4))
+        return QKQ_ERR_ALIGN;
+    const size_t bytes = static_cast<size_t>(T) * Hq * d_h * 2;
+    if (q != out && overlaps(q, bytes, out, bytes)) return QKQ_ERR_ARG;
+    if (workspace == nullptr || workspace_bytes < qkq::attention_kv8_workspace(T, B, Hq, Hkv, d_h)) return QKQ_ERR_WORKSPACE;
+    DeviceInfo dev;
+    rc = current_device(&dev);
+    if (rc) return rc;
+    p.q = static_cast<const uint16_t *>(q);
+    p.half = dtype == QKQ_DTYPE_FP16;
+    p.k_codes = k_codes;
+    p.v_codes = v_codes;
+    p.k_steps = k_steps;
+    p.v_steps = v_steps;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.ratio = Hq / Hkv;
+    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    p.window = window;
+    p.sinks = sinks;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.workspace = workspace;
+    p.status = status;
+    return from_cuda(qkq::attention_kv8_launch(p, d_h, dev, stream));
 }
 
 int qkq_selftest_bounded_wait(unsigned long long limit_ns, int *status, qkq_stream_t stream)

@@ -1,0 +1,482 @@
+// Attention over the paged 8-bit cache for few query rows per sequence: one decoding token, a
+// handful of drafted ones.
+//
+// out[t][h] = sum_j p_j vs_j vc_j / sum_j p_j,  p_j = 2^(s_j - m),  s_j = scale log2(e) ks_j (q . kc_j)
+// over the cached tokens j that query t may see (j <= its index; with a window W also
+// j > index - W or j < sinks); kc, vc the e4m3 codes, ks, vs their page's steps.
+//
+// Memory bound: the codes of every visible cached token are read once, 2 d_h bytes per key head.
+// Each warp takes slices of 16 cached tokens of one key head against up to 8 NT query rows
+// (tokens x heads of the key head), the products as warp-level fp16 MMAs (m16n8k16, fp32 sums)
+// with the cached tokens on the wide side, so a decoding step's few rows waste little:
+//   S^T [16 tokens x rows]  = K [16 x d_h] Q^T,   O^T [d_h x rows] += V^T [d_h x 16] P^T.
+// Codes go from global memory straight into the A fragments: a lane's 16-byte loads hold the
+// channels (K) or channel x token pairs (V) that its fragment needs, which channel stands at which
+// index being free as long as both operands agree; e4m3 -> fp16 is one exact conversion per pair.
+// Queries are scaled by a power of two per row into fp16's range (bf16's 8 bits fit its 11).  P is
+// rounded to fp16 (relative 2^-12); sums, maxima and the output stay fp32.  The page's value step
+// goes into the exponent, w_j = p_j vs_j = 2^(s_j + log2 vs_j - m), so that m bounds what is
+// rounded, and the row sum takes w_j / vs_j.  The running maximum moves only when a logit passes it
+// by more than 2^8 (fp16 and fp32 hold that), which leaves most slices without any exchange.
+//
+// Work split: the slices of all (sequence, query block, key head) in one line, cut into equal
+// parts, one per CTA of a persistent grid, found from the lengths on the device: ragged batches
+// balance without the host knowing a length.  What a part shares with its neighbours goes to the
+// workspace as (rows, maximum, sum) and a second kernel joins it in a fixed order.
+#include "attention_kv8.cuh"
+
+namespace qkq {
+
+namespace {
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// One slice's codes and steps as this lane holds them.
+template <int DH>
+struct Slice {
+    uint32_t k[2][DH / 16];  // tokens g, g + 8: channels 16 t .. of each 64
+    uint32_t v[4][DH / 32];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9: channels g * DH / 8 ..
+    float ks, vs;
+};
+
+template <int DH>
+__device__ __forceinline__ void load_slice(Slice<DH> &s, const AttnKV8Params &p, int page, int hk, int tok0, int g,
+                                           int t)
+{
+    const int pg = page < 0 ? 0 : page;
+    const int64_t ph = static_cast<int64_t>(pg) * p.Hkv + hk;
+    const int64_t base = ((ph << p.x.page_shift) + (tok0 & ((1 << p.x.page_shift) - 1))) * DH;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < DH / 64; ++c) {
+            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p.k_codes + base + (g + 8 * r) * DH + 64 * c + 16 * t));
+            s.k[r][4 * c] = w.x;
+            s.k[r][4 * c + 1] = w.y;
+            s.k[r][4 * c + 2] = w.z;
+            s.k[r][4 * c + 3] = w.w;
+        }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint8_t *src = p.v_codes + base + (2 * t + (r & 1) + 8 * (r >> 1)) * DH + g * (DH / 8);
+        if (DH == 128) {
+            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(src));
+            s.v[r][0] = w.x;
+            s.v[r][1] = w.y;
+            s.v[r][DH / 32 - 2] = w.z;
+            s.v[r][DH / 32 - 1] = w.w;
+        } else {
+            const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(src));
+            s.v[r][0] = w.x;
+            s.v[r][1] = w.y;
+        }
+    }
+    s.ks = kv8_step(p.k_steps, ph);
+    s.vs = kv8_step(p.v_steps, ph);
+}
+
+template <int DH, int NT, int NW>
+struct MergeSmem {
+    float o[NW][8 * NT][DH];
+    float m[NW][8 * NT], l[NW][8 * NT];
+};
+
+template <int DH, int NT, int NW>
+__global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p)
+{
+    constexpr int R = 8 * NT;     // query rows of a unit
+    constexpr int KS = DH / 16;   // K-steps of S, M tiles of O
+    __shared__ __align__(16) MergeSmem<DH, NT, NW> sm;
+    __shared__ KV8Start s_start;
+    wait_prior_grid();
+    allow_next_grid();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const KV8Index &x = p.x;
+    const KV8Partials part(p.workspace, gridDim.x, R, DH);
+
+    find_start<16, R, NW * 32>(p, s_start);
+    int64_t cur = s_start.lo;
+    const int64_t hi = s_start.hi;
+    int b = s_start.b, qt = s_start.qt, hk = s_start.hk;
+    int j0 = s_start.j0;
+    if (threadIdx.x == 0) part.meta[blockIdx.x] = KV8Meta{cur, hi > cur ? j0 : 0, b, qt, hk};
+    int flags = s_start.flags;
+    bool first = true;
+
+    while (cur < hi) {
+        const KV8Seq s = kv8_seq_checked(x, b);
+        const KV8Span span = unit_span<16>(p, s, qt, R);
+        const int j1 = static_cast<int>(min(static_cast<int64_t>(span.count), j0 + (hi - cur)));
+        const int rows = min(R, s.n * p.ratio - qt * R);
+
+        // ---- this unit's queries: B fragments, scaled per row into fp16 --------------------
+        uint32_t qf[NT][KS][2];
+        float fac[NT][2];   // rows 2t, 2t + 1 of each n-tile: scale log2(e) / the row's factor
+        int at[NT][2];      // their index in the sequence (none: -1)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = 8 * n + g;
+            float f = 0.0f;
+            float2 v[KS][2];
+            float amax = 0.0f;
+            if (row < rows) {
+                const int rr = qt * R + row;
+                const uint16_t *src = p.q + (static_cast<int64_t>(s.q0 + rr / p.ratio) * p.Hq + hk * p.ratio + rr % p.ratio) * DH;
+#pragma unroll
+                for (int c = 0; c < DH / 64; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 64 * c + 16 * t + 8 * h));
+                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[4 * c + 2 * h + (e >> 1)][e & 1] = unpack16(u[e], p.half);
+                    }
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        amax = fmaxf(amax, fabsf(v[k][e].x) <= 3.402823466e38f ? fabsf(v[k][e].x) : 0.0f);
+                        amax = fmaxf(amax, fabsf(v[k][e].y) <= 3.402823466e38f ? fabsf(v[k][e].y) : 0.0f);
+                    }
+            } else {
+#pragma unroll
+                for (int k = 0; k < KS; ++k) v[k][0] = v[k][1] = make_float2(0.0f, 0.0f);
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, 2));
+            const int e = row_exponent(amax);
+            const float up = exp2i(-e);
+            f = p.scale_log2 * exp2i(e);
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) qf[n][k][h] = pack16(v[k][h].x * up, v[k][h].y * up, true);
+            const int idx = row < rows ? s.len - s.n + (qt * R + row) / p.ratio : -1;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                fac[n][c] = __shfl_sync(FULL_MASK, f, (2 * t + c) * 4);
+                at[n][c] = __shfl_sync(FULL_MASK, idx, (2 * t + c) * 4);
+            }
+        }
+
+        float o[NT][KS][4];
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][k][e] = 0.0f;
+        }
+
+        // ---- the warp's slices -------------------------------------------------------------
+        auto token = [&](int j) { return 16 * (j < span.head ? j : j + span.skip); };
+        auto page_of = [&](int j) {
+            const int tok = token(j);
+            if (j >= j1) return -1;
+            if (tok >= s.len) return -1;
+            const int id = kv8_page(x, b, tok >> x.page_shift);
+            if (id < 0) flags |= ST_CACHE_INDEX;
+            return id;
+        };
+        Slice<DH> sl;
+        int j = j0 + warp;
+        int page = page_of(j);
+        if (j < j1) load_slice<DH>(sl, p, page, hk, token(j), g, t);
+        int page_next = page_of(j + NW);
+        for (; j < j1; j += NW) {
+            const int tok0 = token(j);
+            float sc[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][e] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const uint32_t a0 = e4m3x2_to_half2(sl.k[0][k] & 0xffffu), a2 = e4m3x2_to_half2(sl.k[0][k] >> 16);
+                const uint32_t a1 = e4m3x2_to_half2(sl.k[1][k] & 0xffffu), a3 = e4m3x2_to_half2(sl.k[1][k] >> 16);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(sc[n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
+            }
+            const float ks = sl.ks, vs = sl.vs, lvs = lg2(vs), ivs = 1.0f / vs;
+            // every row sees every token of the slice?
+            const bool full = page >= 0 && tok0 + 15 <= span.first &&
+                              (p.window == 0 || tok0 > span.last - p.window || tok0 + 15 < p.sinks);
+            bool passes = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sc[n][e] = __fmaf_rn(sc[n][e], fac[n][e & 1] * ks, lvs);
+                    if (!full) {
+                        const int tok = tok0 + g + 8 * (e >> 1);
+                        const int i = at[n][e & 1];
+                        const bool see = page >= 0 && tok <= i && (p.window == 0 || tok > i - p.window || tok < p.sinks);
+                        if (!see) sc[n][e] = -INFINITY;
+                    }
+                    passes |= sc[n][e] > m[n][e & 1] + 8.0f;
+                }
+            if (__any_sync(FULL_MASK, passes)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float top = fmaxf(sc[n][c], sc[n][2 + c]);
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, off));
+                        top = fmaxf(top, m[n][c]);
+                        const float alpha = m[n][c] == top ? 1.0f : ex2(m[n][c] - top);
+                        m[n][c] = top;
+                        l[n][c] *= alpha;
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            o[n][k][c] *= alpha;
+                            o[n][k][2 + c] *= alpha;
+                        }
+                    }
+            }
+            uint32_t pb[NT][2], see01[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = ex2(sc[n][e] - (m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1]));
+                l[n][0] = __fmaf_rn(w[0] + w[2], ivs, l[n][0]);
+                l[n][1] = __fmaf_rn(w[1] + w[3], ivs, l[n][1]);
+                pb[n][0] = transpose8x8(pack16(w[0], w[1], true));
+                pb[n][1] = transpose8x8(pack16(w[2], w[3], true));
+            }
+            uint32_t bad[4][DH / 32];
+            bool any_bad = false;
+            if (!full) {
+                // NaN value codes in a slice that some row does not see wholly: a masked one must
+                // not reach the sums (0 * NaN), a visible one must
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int w = 0; w < DH / 32; ++w) {
+                        const uint32_t nb = e4m3_nan_bits(sl.v[r][w]) >> 7;
+                        bad[r][w] = nb * 0x38u;  // 1.0 where NaN
+                        sl.v[r][w] &= ~(nb * 0xffu);
+                        any_bad |= nb != 0;
+                    }
+                any_bad = __any_sync(FULL_MASK, any_bad);
+                if (any_bad) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        see01[n][0] = transpose8x8(pack16(sc[n][0] == -INFINITY ? 0.0f : 1.0f, sc[n][1] == -INFINITY ? 0.0f : 1.0f, true));
+                        see01[n][1] = transpose8x8(pack16(sc[n][2] == -INFINITY ? 0.0f : 1.0f, sc[n][3] == -INFINITY ? 0.0f : 1.0f, true));
+                    }
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < DH / 32; ++w) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // channels (4w + 2h, 4w + 2h + 1) of the lane's run: rows g and g + 8 of M tile 2w + h
+                    const uint32_t lo = __byte_perm(sl.v[0][w], sl.v[1][w], h ? 0x7362 : 0x5140);
+                    const uint32_t up = __byte_perm(sl.v[2][w], sl.v[3][w], h ? 0x7362 : 0x5140);
+                    const uint32_t a0 = e4m3x2_to_half2(lo & 0xffffu), a1 = e4m3x2_to_half2(lo >> 16);
+                    const uint32_t a2 = e4m3x2_to_half2(up & 0xffffu), a3 = e4m3x2_to_half2(up >> 16);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16(o[n][2 * w + h], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                }
+            }
+            if (any_bad) {
+#pragma unroll
+                for (int w = 0; w < DH / 32; ++w)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t lo = __byte_perm(bad[0][w], bad[1][w], h ? 0x7362 : 0x5140);
+                        const uint32_t up = __byte_perm(bad[2][w], bad[3][w], h ? 0x7362 : 0x5140);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            mma_f16(d, e4m3x2_to_half2(lo & 0xffffu), e4m3x2_to_half2(lo >> 16), e4m3x2_to_half2(up & 0xffffu),
+                                    e4m3x2_to_half2(up >> 16), see01[n][0], see01[n][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (d[e] > 0.0f) o[n][2 * w + h][e] = __uint_as_float(0x7fc00000u);
+                        }
+                    }
+            }
+            page = page_next;
+            if (j + NW < j1) load_slice<DH>(sl, p, page, hk, token(j + NW), g, t);
+            page_next = page_of(j + 2 * NW);
+        }
+
+        // ---- join the warps ------------------------------------------------------------------
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float sum = l[n][c];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(FULL_MASK, sum, off);
+                const int row = 8 * n + 2 * t + c;
+                if (row < rows) {
+                    if (g == 0) {
+                        sm.m[warp][row] = m[n][c];
+                        sm.l[warp][row] = sum;
+                    }
+#pragma unroll
+                    for (int k = 0; k < KS; k += 2)
+                        *reinterpret_cast<float4 *>(&sm.o[warp][row][g * (DH / 8) + 2 * k]) =
+                            make_float4(o[n][k][c], o[n][k][2 + c], o[n][k + 1][c], o[n][k + 1][2 + c]);
+                }
+            }
+        __syncthreads();
+        const bool whole = j0 == 0 && j1 == span.count;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first ? 0 : 1);
+        for (int i = threadIdx.x; i < rows * (DH / 4); i += NW * 32) {
+            const int row = i / (DH / 4), c = 4 * (i % (DH / 4));
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) top = fmaxf(top, sm.m[w][row]);
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = sm.m[w][row] == -INFINITY ? 0.0f : ex2(sm.m[w][row] - top);
+                const float4 v = *reinterpret_cast<const float4 *>(&sm.o[w][row][c]);
+                if (sm.m[w][row] == -INFINITY && sm.l[w][row] == 0.0f) continue;
+                sum = __fmaf_rn(sm.l[w][row], f, sum);
+                acc.x = __fmaf_rn(v.x, f, acc.x);
+                acc.y = __fmaf_rn(v.y, f, acc.y);
+                acc.z = __fmaf_rn(v.z, f, acc.z);
+                acc.w = __fmaf_rn(v.w, f, acc.w);
+            }
+            if (whole) {
+                store_row(p, s, qt * R + row, hk, c, DH, acc, top, sum);
+            } else {
+                *reinterpret_cast<float4 *>(part.o + (slot * R + row) * DH + c) = acc;
+                if (c == 0) *reinterpret_cast<float2 *>(part.ml + (slot * R + row) * 2) = make_float2(top, sum);
+            }
+        }
+        cur += j1 - j0;
+        first = false;
+        j0 = 0;
+        if (j1 == span.count && cur < hi) next_unit(p, s, R, b, qt, hk);
+    }
+    if (p.status) {
+        flags = __reduce_or_sync(FULL_MASK, flags);
+        if (flags && lane == 0) atomicOr(p.status, flags);
+    }
+}
+
+// Joins the partial rows of the units that a boundary between two CTAs cuts.  CTA (i, row):
+// boundary i opens the unit's second part, or does nothing.
+template <int DH>
+__global__ void __launch_bounds__(256) k_attention_kv8_join(const AttnKV8Params p, int ctas, int R)
+{
+    constexpr int G = 256 / (DH / 4);  // partials taken side by side
+    __shared__ float s_m[256], s_l[G];
+    __shared__ __align__(16) float s_o[G][DH];
+    wait_prior_grid();
+    const KV8Partials part(p.workspace, ctas, R, DH);
+    const int i = blockIdx.x + 1;
+    const KV8Meta me = part.meta[i];
+    if (me.j0 == 0) return;
+    const int64_t u0 = me.lo - me.j0;
+    const KV8Meta prev = part.meta[i - 1];
+    if (prev.lo > u0) return;
+    const KV8Seq s = kv8_seq_checked(p.x, me.b);
+    const int row = blockIdx.y;
+    if (me.qt * R + row >= s.n * p.ratio) return;
+    int count = 2;  // CTA i - 1, i, and those that go on with the unit
+    while (i - 1 + count < ctas) {
+        const KV8Meta c = part.meta[i - 1 + count];
+        if (c.j0 == 0 || c.lo - c.j0 != u0) break;
+        ++count;
+    }
+    auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(i - 1) + (prev.lo == u0 ? 0 : 1) : 2 * static_cast<int64_t>(i - 1 + k); };
+    float top = -INFINITY;
+    for (int k = threadIdx.x; k < count; k += 256) top = fmaxf(top, part.ml[(slot(k) * R + row) * 2]);
+    s_m[threadIdx.x] = top;
+    __syncthreads();
+    for (int o = 128; o; o >>= 1) {
+        if (threadIdx.x < o) s_m[threadIdx.x] = fmaxf(s_m[threadIdx.x], s_m[threadIdx.x + o]);
+        __syncthreads();
+    }
+    top = s_m[0];
+    const int grp = threadIdx.x / (DH / 4), c = 4 * (threadIdx.x % (DH / 4));
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int k = grp; k < count; k += G) {
+        const float2 ml = *reinterpret_cast<const float2 *>(part.ml + (slot(k) * R + row) * 2);
+        const float4 v = *reinterpret_cast<const float4 *>(part.o + (slot(k) * R + row) * DH + c);
+        if (ml.x == -INFINITY && ml.y == 0.0f) continue;
+        const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+        sum = __fmaf_rn(ml.y, f, sum);
+        acc.x = __fmaf_rn(v.x, f, acc.x);
+        acc.y = __fmaf_rn(v.y, f, acc.y);
+        acc.z = __fmaf_rn(v.z, f, acc.z);
+        acc.w = __fmaf_rn(v.w, f, acc.w);
+    }
+    *reinterpret_cast<float4 *>(&s_o[grp][c]) = acc;
+    if (c == 0) s_l[grp] = sum;
+    __syncthreads();
+    if (grp == 0) {
+#pragma unroll
+        for (int k = 1; k < G; ++k) {
+            const float4 v = *reinterpret_cast<const float4 *>(&s_o[k][c]);
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+        sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < G; ++k) sum += s_l[k];
+        store_row(p, s, me.qt * R + row, me.hk, c, DH, acc, top, sum);
+    }
+}
+
+template <int DH, int NT>
+cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t stream)
+{
+    constexpr int NW = 4;
+    const int ctas = dev.num_sms * 3 < KV8_MAX_CTAS ? dev.num_sms * 3 : KV8_MAX_CTAS;
+    cudaError_t e = launch_after_prior(k_attention_kv8<DH, NT, NW>, dim3(ctas), dim3(NW * 32), 0, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_after_prior(k_attention_kv8_join<DH>, dim3(ctas - 1, 8 * NT), dim3(256), 0, stream, p, ctas, 8 * NT);
+}
+
+}  // namespace
+
+size_t attention_kv8_workspace(int64_t T, int B, int Hq, int Hkv, int d_h)
+{
+    if (T <= 0 || B <= 0) return 0;
+    return KV8Partials::bytes(KV8_MAX_CTAS, 16, d_h);
+}
+
+cudaError_t attention_kv8_launch(const AttnKV8Params &p, int d_h, const DeviceInfo &dev, cudaStream_t stream)
+{
+    const bool two = p.x.cu != nullptr || p.ratio > 8;
+    cudaError_t e;
+    if (d_h == 64)
+        e = two ? launch<64, 2>(p, dev, stream) : launch<64, 1>(p, dev, stream);
+    else
+        e = two ? launch<128, 2>(p, dev, stream) : launch<128, 1>(p, dev, stream);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace qkq

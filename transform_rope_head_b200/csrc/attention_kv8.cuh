@@ -1,0 +1,225 @@
+// What the kernels of the attention over the paged 8-bit cache share: the work line and how a CTA
+// finds its part of it, the partial rows that parts of a unit leave, and the output rows.
+#pragma once
+
+#include <math.h>
+
+#include "kv8.cuh"
+
+namespace qkq {
+
+constexpr int KV8_MAX_CTAS = 512;  // above the persistent grids here (148 SMs x 3)
+
+// Where a CTA's part begins: its first unit continues at tile j0 of (b, qt, hk).
+struct KV8Meta {
+    int64_t lo;
+    int j0, b, qt, hk;
+};
+
+// The workspace: per CTA its beginning, and two partial units (its first, and its last where that is
+// another one), each R rows of unnormalised outputs with (maximum, sum).
+struct KV8Partials {
+    KV8Meta *meta;
+    float *ml, *o;
+    static constexpr size_t META = 32;
+    __host__ __device__ KV8Partials(void *ws, int ctas, int rows, int d_h)
+    {
+        char *c = static_cast<char *>(ws);
+        meta = reinterpret_cast<KV8Meta *>(c);
+        ml = reinterpret_cast<float *>(c + META * ctas);
+        o = ml + static_cast<size_t>(ctas) * 2 * rows * 2;
+    }
+    static size_t bytes(int ctas, int rows, int d_h)
+    {
+        return ctas * (META + static_cast<size_t>(2) * rows * (2 + d_h) * sizeof(float));
+    }
+};
+static_assert(sizeof(KV8Meta) <= KV8Partials::META, "workspace layout");
+
+// A sequence whose rows lie outside the buffers has none; one whose length does has no cached
+// tokens (its rows come out empty).
+__device__ __forceinline__ KV8Seq kv8_seq_checked(const KV8Index &x, int b)
+{
+    KV8Seq s = kv8_seq(x, b);
+    if (!s.ok) {
+        const bool rows = s.q0 >= 0 && s.n >= 0 && static_cast<int64_t>(s.q0) + s.n <= x.T;
+        if (!rows) s.n = 0;
+        s.len = 0;
+    }
+    return s;
+}
+
+// Tiles of TS cached tokens that some row of a unit (rows qt * R ..) sees: tile j of the unit is
+// tile j of the sequence for j < head, j + skip after.
+struct KV8Span {
+    int count, head, skip;
+    int first, last;  // index in the sequence of the first and last row's token
+};
+
+template <int TS>
+__device__ __forceinline__ KV8Span unit_span(const AttnKV8Params &p, const KV8Seq &s, int qt, int R)
+{
+    KV8Span u;
+    const int r0 = qt * R, r1 = min(r0 + R, s.n * p.ratio) - 1;
+    u.first = s.len - s.n + r0 / p.ratio;
+    u.last = s.len - s.n + r1 / p.ratio;
+    const int end = max(u.last + 1, 0);  // <= len
+    const int lo = p.window > 0 ? max(u.first - p.window + 1, 0) : 0;
+    const int sink = p.window > 0 ? (min(p.sinks, end) + TS - 1) / TS : 0;
+    const int w0 = min(lo, end) / TS, w1 = (end + TS - 1) / TS;
+    if (w0 > sink) {
+        u.head = sink;
+        u.skip = w0 - sink;
+        u.count = sink + w1 - w0;
+    } else {
+        u.head = w1;
+        u.skip = 0;
+        u.count = w1;
+    }
+    u.count = max(u.count, 1);  // a unit without tokens still writes its rows
+    return u;
+}
+
+__device__ __forceinline__ int unit_blocks(const AttnKV8Params &p, const KV8Seq &s, int R)
+{
+    return (s.n * p.ratio + R - 1) / R;
+}
+
+template <int TS>
+__device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, const KV8Seq &s, int R)
+{
+    int64_t w = 0;
+    const int blocks = unit_blocks(p, s, R);
+    for (int q = 0; q < blocks; ++q) w += unit_span<TS>(p, s, q, R).count;
+    return w * p.Hkv;
+}
+
+struct KV8Start {
+    int64_t lo, hi, total, base;
+    int b, qt, hk, j0, flags;
+    int64_t warp_sum[32];
+};
+
+// The CTA's part [lo, hi) of the line of all tiles (sequence, query block, key head, tile), and the
+// unit that holds lo.  Every thread of the CTA calls it.
+template <int TS, int R, int THREADS>
+__device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st)
+{
+    constexpr int NWARP = THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int B = p.x.B;
+    int64_t sum = 0;
+    int bad = 0;
+    for (int b = threadIdx.x; b < B; b += THREADS) {
+        bad |= !kv8_seq(p.x, b).ok;
+        sum += seq_tiles<TS>(p, kv8_seq_checked(p.x, b), R);
+    }
+    const int64_t mine = sum;  // of the only sequence, when there are no more than threads
+    bad = __syncthreads_or(bad);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+    if (lane == 0) st.warp_sum[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < NWARP; ++w) total += st.warp_sum[w];
+    __syncthreads();
+    // parts of at least one tile a warp
+    const int64_t least = (total + NWARP - 1) / NWARP;
+    const int64_t parts = least < static_cast<int64_t>(gridDim.x) ? least : gridDim.x;
+    const int64_t id = blockIdx.x;
+    const int64_t lo = id < parts ? total / parts * id + total % parts * id / parts : total;
+    const int64_t hi = id < parts ? total / parts * (id + 1) + total % parts * (id + 1) / parts : total;
+    if (threadIdx.x == 0) {
+        st.lo = lo;
+        st.hi = hi;
+        st.total = total;
+        st.b = st.qt = st.hk = st.j0 = 0;
+        st.flags = bad ? ST_CACHE_INDEX : 0;
+        st.base = 0;
+    }
+    if (lo >= hi) {
+        __syncthreads();
+        return;
+    }
+    int64_t base = 0;
+    for (int b0 = 0; b0 < B; b0 += THREADS) {
+        const int b = b0 + threadIdx.x;
+        const int64_t w = B <= THREADS ? mine : b < B ? seq_tiles<TS>(p, kv8_seq_checked(p.x, b), R) : 0;
+        int64_t inc = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(FULL_MASK, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) st.warp_sum[warp] = inc;
+        __syncthreads();
+        int64_t before = base;
+#pragma unroll
+        for (int k = 0; k < NWARP; ++k) {
+            if (k < warp) before += st.warp_sum[k];
+            base += st.warp_sum[k];
+        }
+        inc += before;
+        if (b < B && lo >= inc - w && lo < inc) {
+            st.b = b;
+            st.base = inc - w;
+        }
+        __syncthreads();
+        if (lo < base) break;
+    }
+    if (threadIdx.x == 0) {
+        const KV8Seq s = kv8_seq_checked(p.x, st.b);
+        int64_t rem = lo - st.base;
+        const int blocks = unit_blocks(p, s, R);
+        for (int q = 0; q < blocks; ++q) {
+            const int c = unit_span<TS>(p, s, q, R).count;
+            if (rem < static_cast<int64_t>(c) * p.Hkv) {
+                st.qt = q;
+                st.hk = static_cast<int>(rem / c);
+                st.j0 = static_cast<int>(rem % c);
+                break;
+            }
+            rem -= static_cast<int64_t>(c) * p.Hkv;
+        }
+    }
+    __syncthreads();
+}
+
+// The unit after (b, qt, hk); there is one.
+__device__ __forceinline__ void next_unit(const AttnKV8Params &p, const KV8Seq &s, int R, int &b, int &qt, int &hk)
+{
+    if (++hk < p.Hkv) return;
+    hk = 0;
+    if (++qt < unit_blocks(p, s, R)) return;
+    qt = 0;
+    do {
+        ++b;
+    } while (b < p.x.B - 1 && kv8_seq_checked(p.x, b).n == 0);
+}
+
+// 2^e of a row's scaling into fp16: the row's largest magnitude goes to [2^14, 2^15), so that
+// what fp16 flushes is 2^-38 of it.
+__device__ __forceinline__ int row_exponent(float amax)
+{
+    const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+    return amax > 0.0f ? max(e, -126) : 0;
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Four channels of row rr of (sequence s, key head hk): the normalised output (0 where the row saw
+// nothing), and with the first ones the row's log-sum-exp.
+__device__ __forceinline__ void store_row(const AttnKV8Params &p, const KV8Seq &s, int rr, int hk, int c, int d_h,
+                                          const float4 &acc, float top, float sum)
+{
+    const int64_t row = static_cast<int64_t>(s.q0 + rr / p.ratio) * p.Hq + hk * p.ratio + rr % p.ratio;
+    const bool empty = top == -INFINITY && sum == 0.0f;
+    const float inv = empty ? 0.0f : 1.0f / sum;
+    uint2 w;
+    w.x = empty ? 0u : pack16(acc.x * inv, acc.y * inv, p.half);
+    w.y = empty ? 0u : pack16(acc.z * inv, acc.w * inv, p.half);
+    *reinterpret_cast<uint2 *>(p.out + row * d_h + c) = w;
+    if (c == 0 && p.lse) p.lse[row] = empty ? -INFINITY : (lg2(sum) + top) * 0.6931471805599453f;
+}
+
+}  // namespace qkq

@@ -196,6 +196,60 @@ cudaError_t attention_scores_tc_launch(const ScoresParams &p, int d_h, int group
 cudaError_t attention_scores_mma_launch(const ScoresParams &p, const DeviceInfo &dev, int d_h,
                                         int group, cudaStream_t stream);
 
+// ---- paged 8-bit cache (KV8) ------------------------------------------------------------
+
+// The batch and its pages.
+struct KV8Index {
+    int64_t T;                  // rows of new tokens
+    const int32_t *cu;          // [B + 1] first row of each sequence, nullable: one token each
+    const int32_t *seq_lens;    // [B] cached tokens, new ones included
+    const int32_t *block_table; // [B][max_pages]
+    int B, max_pages;
+    int64_t num_pages;
+    int page_shift;             // log2 of the tokens per page
+};
+
+struct AppendKV8Params {
+    KV8Index x;
+    const uint16_t *q;          // nullable
+    const uint16_t *k, *v;      // rows of [heads][d_h], strides in elements
+    int64_t q_stride, k_stride, v_stride;
+    bool half;                  // fp16 instead of bf16
+    const int32_t *pos;         // nullable: the index in the sequence
+    int Hq, Hkv;
+    int rot;                    // rotated channels (a multiple of 16; 0: none)
+    bool interleaved;
+    const float *cos_t, *sin_t; // [max_pos][rot / 2]
+    int max_pos;
+    uint16_t *q_out;
+    uint8_t *k_codes, *v_codes;
+    float *k_steps, *v_steps;
+    int *status;                // nullable
+    int64_t slots;              // filled by the launcher
+    unsigned kv_ctas;           // filled by the launcher
+};
+
+cudaError_t append_kv8_launch(AppendKV8Params p, int d_h, cudaStream_t stream);
+
+struct AttnKV8Params {
+    KV8Index x;
+    const uint16_t *q;          // [T][Hq][d_h]
+    bool half;
+    const uint8_t *k_codes, *v_codes;
+    const float *k_steps, *v_steps;
+    int Hq, Hkv, ratio;
+    float scale_log2;           // softmax scale * log2(e)
+    int window, sinks;          // window 0: none
+    uint16_t *out;              // [T][Hq][d_h]
+    float *lse;                 // [T][Hq], nullable
+    void *workspace;
+    int *status;                // nullable
+};
+
+size_t attention_kv8_workspace(int64_t T, int B, int Hq, int Hkv, int d_h);
+cudaError_t attention_kv8_launch(const AttnKV8Params &p, int d_h, const DeviceInfo &dev,
+                                 cudaStream_t stream);
+
 // ---- test hook: the error path of the time-bounded waits ------------------------------
 
 cudaError_t bounded_wait_selftest_launch(unsigned long long limit_ns, int *status,
