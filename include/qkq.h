@@ -382,8 +382,8 @@ int qkq_attention_scores_mma(const void *q_bf16, int64_t Tq, const uint8_t *k_co
  *   [0, num_pages), a length above max_pages * page_size or a row range outside [0, T) sets
  *   QKQ_STATUS_CACHE_INDEX and that page or sequence is left out; nothing outside the buffers is
  *   read or written.
- *   Supported: d_h in {64, 128}, page_size in {16, 32, 64, 128}, bf16 or fp16 tensors, any
- *   Hq that is a multiple of Hkv.  16-byte aligned q, k, v, q_out, out, codes, tables, workspace.
+ *   Supported: d_h in {64, 128}, page_size in {16, 32, 64, 128}, max_pages * page_size <= 2^30,
+ *   bf16 or fp16 tensors, any Hq that is a multiple of Hkv.  16-byte aligned q, k, v, q_out, out, codes, tables, workspace.
  */
 
 /*

@@ -78,7 +78,7 @@ def _append(**over):
     (dict(out=None), -1), (dict(q=None), -1), (dict(cos=None), -1), (dict(lens=None), -1), (dict(table=None), -1),
     (dict(style=2), -1), (dict(style=0x100), -5),
     (dict(d=96), -2), (dict(d=256), -2), (dict(ps=8), -2), (dict(ps=48), -2), (dict(ps=256), -2), (dict(Hq=7), -2),
-    (dict(Hkv=0), -2), (dict(T=-1), -2), (dict(B=-1), -2), (dict(mp=0), -2), (dict(P=0), -2), (dict(cu=None), -2),
+    (dict(Hkv=0), -2), (dict(T=-1), -2), (dict(B=-1), -2), (dict(mp=0), -2), (dict(mp=2 ** 26 + 1), -2), (dict(P=0), -2), (dict(cu=None), -2),
     (dict(rot=8), -2), (dict(rot=80), -2), (dict(rot=-16), -2), (dict(max_pos=0), -2), (dict(T=2 ** 31), -2),
     (dict(ks=64), -2), (dict(ks=132), -2), (dict(qs=100), -2), (dict(vs=127), -2),
     (dict(k=0x200008), -3), (dict(out=0x600008), -3), (dict(vc=0x800004), -3), (dict(cos=0x500004), -3),

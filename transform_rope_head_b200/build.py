@@ -34,7 +34,7 @@ def _units():
     units = [("api.cu", []), ("moments.cu", []), ("moments_noalloc.cu", []), ("solve.cu", []),
              ("dequant_f32.cu", []),
              ("attention_scores.cu", []), ("attention_scores_tc.cu", []),
-             ("attention_scores_mma.cu", []), ("append_kv8.cu", []), ("attention_kv8.cu", []),
+             ("attention_scores_mma.cu", []), ("append_kv8.cu", []), ("attention_kv8.cu", []), ("attention_kv8_tc.cu", []),
              ("selftest.cu", [])]
     for dh in (64, 128):
         for st in (0, 1):

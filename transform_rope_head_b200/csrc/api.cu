@@ -136,6 +136,7 @@ int kv8_index(int64_t T, const int32_t *cu_new, const int32_t *seq_lens, int B, 
     if (Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || Hq > 65536) return QKQ_ERR_SHAPE;
     if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return QKQ_ERR_SHAPE;
     if (max_pages < 1 || num_pages < 1 || num_pages > INT32_MAX) return QKQ_ERR_SHAPE;
+    if (static_cast<int64_t>(max_pages) * page_size > 1 << 30) return QKQ_ERR_SHAPE;  // 32-bit token indices
     if (!cu_new && T != B) return QKQ_ERR_SHAPE;
     if (T * (Hq / Hkv) > INT32_MAX) return QKQ_ERR_SHAPE;  // 32-bit query row indices
     if (T == 0 || B == 0) return QKQ_OK;
@@ -682,8 +683,9 @@ int qkq_attention_kv8(const void *q, int dtype, int64_t T, const int32_t *cu_new
     p.Hkv = Hkv;
     p.ratio = Hq / Hkv;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    p.window = window;
-    p.sinks = sinks;
+    // a window as long as the longest sequence hides nothing
+    p.window = window < static_cast<int64_t>(max_pages) * page_size ? window : 0;
+    p.sinks = sinks < (1 << 30) ? sinks : 1 << 30;
     p.out = static_cast<uint16_t *>(out);
     p.lse = lse;
     p.workspace = workspace;

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p
     const KV8Index &x = p.x;
     const KV8Partials part(p.workspace, gridDim.x, R, DH);
 
-    find_start<16, R, NW * 32>(p, s_start);
+    find_start<16, R, NW * 32>(p, s_start, NW);  // at least a slice per warp
     int64_t cur = s_start.lo;
     const int64_t hi = s_start.hi;
     int b = s_start.b, qt = s_start.qt, hk = s_start.hk;
@@ -450,26 +450,83 @@ __global__ void __launch_bounds__(256) k_attention_kv8_join(const AttnKV8Params 
     }
 }
 
+// The same for units of many rows and few parts: 1024 / DH rows side by side.
+template <int DH>
+__global__ void __launch_bounds__(256) k_attention_kv8_join_rows(const AttnKV8Params p, int ctas, int R)
+{
+    wait_prior_grid();
+    const KV8Partials part(p.workspace, ctas, R, DH);
+    const int i = blockIdx.x + 1;
+    const KV8Meta me = part.meta[i];
+    if (me.j0 == 0) return;
+    const int64_t u0 = me.lo - me.j0;
+    const KV8Meta prev = part.meta[i - 1];
+    if (prev.lo > u0) return;
+    const KV8Seq s = kv8_seq_checked(p.x, me.b);
+    const int rows = min(R, s.n * p.ratio - me.qt * R);
+    int count = 2;
+    while (i - 1 + count < ctas) {
+        const KV8Meta c = part.meta[i - 1 + count];
+        if (c.j0 == 0 || c.lo - c.j0 != u0) break;
+        ++count;
+    }
+    auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(i - 1) + (prev.lo == u0 ? 0 : 1) : 2 * static_cast<int64_t>(i - 1 + k); };
+    constexpr int G = 256 / (DH / 4);
+    const int c = 4 * (threadIdx.x % (DH / 4));
+    for (int row = blockIdx.y * G + threadIdx.x / (DH / 4); row < rows; row += gridDim.y * G) {
+        float top = -INFINITY;
+        for (int k = 0; k < count; ++k) top = fmaxf(top, part.ml[(slot(k) * R + row) * 2]);
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float sum = 0.0f;
+        for (int k = 0; k < count; ++k) {
+            const float2 ml = *reinterpret_cast<const float2 *>(part.ml + (slot(k) * R + row) * 2);
+            const float4 v = *reinterpret_cast<const float4 *>(part.o + (slot(k) * R + row) * DH + c);
+            if (ml.x == -INFINITY && ml.y == 0.0f) continue;
+            const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+            sum = __fmaf_rn(ml.y, f, sum);
+            acc.x = __fmaf_rn(v.x, f, acc.x);
+            acc.y = __fmaf_rn(v.y, f, acc.y);
+            acc.z = __fmaf_rn(v.z, f, acc.z);
+            acc.w = __fmaf_rn(v.w, f, acc.w);
+        }
+        store_row(p, s, me.qt * R + row, me.hk, c, DH, acc, top, sum);
+    }
+}
+
 template <int DH, int NT>
 cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t stream)
 {
     constexpr int NW = 4;
     const int ctas = dev.num_sms * 3 < KV8_MAX_CTAS ? dev.num_sms * 3 : KV8_MAX_CTAS;
-    cudaError_t e = launch_after_prior(k_attention_kv8<DH, NT, NW>, dim3(ctas), dim3(NW * 32), 0, stream, p);
+    const cudaError_t e = launch_after_prior(k_attention_kv8<DH, NT, NW>, dim3(ctas), dim3(NW * 32), 0, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_after_prior(k_attention_kv8_join<DH>, dim3(ctas - 1, 8 * NT), dim3(256), 0, stream, p, ctas, 8 * NT);
+    return attention_kv8_join_launch(p, DH, ctas, 8 * NT, stream);
 }
 
 }  // namespace
 
+cudaError_t attention_kv8_join_launch(const AttnKV8Params &p, int d_h, int ctas, int R, cudaStream_t stream)
+{
+    if (R <= 32) {
+        const dim3 grid(ctas - 1, R);
+        return d_h == 64 ? launch_after_prior(k_attention_kv8_join<64>, grid, dim3(256), 0, stream, p, ctas, R)
+                         : launch_after_prior(k_attention_kv8_join<128>, grid, dim3(256), 0, stream, p, ctas, R);
+    }
+    const dim3 grid(ctas - 1, 8);
+    return d_h == 64 ? launch_after_prior(k_attention_kv8_join_rows<64>, grid, dim3(256), 0, stream, p, ctas, R)
+                     : launch_after_prior(k_attention_kv8_join_rows<128>, grid, dim3(256), 0, stream, p, ctas, R);
+}
+
 size_t attention_kv8_workspace(int64_t T, int B, int Hq, int Hkv, int d_h)
 {
     if (T <= 0 || B <= 0) return 0;
-    return KV8Partials::bytes(KV8_MAX_CTAS, 16, d_h);
+    return kv8_takes_tc(T, B, Hq / Hkv) ? KV8Partials::bytes(KV8_TC_MAX_CTAS, KV8_TC_ROWS, d_h)
+                                        : KV8Partials::bytes(KV8_MAX_CTAS, 16, d_h);
 }
 
 cudaError_t attention_kv8_launch(const AttnKV8Params &p, int d_h, const DeviceInfo &dev, cudaStream_t stream)
 {
+    if (kv8_takes_tc(p.x.T, p.x.B, p.ratio)) return attention_kv8_tc_launch(p, d_h, dev, stream);
     const bool two = p.x.cu != nullptr || p.ratio > 8;
     cudaError_t e;
     if (d_h == 64)

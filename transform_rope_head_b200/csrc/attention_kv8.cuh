@@ -85,36 +85,54 @@ __device__ __forceinline__ int unit_blocks(const AttnKV8Params &p, const KV8Seq 
     return (s.n * p.ratio + R - 1) / R;
 }
 
+// Tiles of a sequence over all its query blocks and key heads; each lane of the warp asks for its own
+// (b < 0: none).  Long lists of blocks are summed by the whole warp.
 template <int TS>
-__device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, const KV8Seq &s, int R)
+__device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, int b, int R, int lane)
 {
     int64_t w = 0;
-    const int blocks = unit_blocks(p, s, R);
-    for (int q = 0; q < blocks; ++q) w += unit_span<TS>(p, s, q, R).count;
+    int blocks = 0;
+    if (b >= 0) {
+        const KV8Seq s = kv8_seq_checked(p.x, b);
+        blocks = unit_blocks(p, s, R);
+        if (blocks <= 2)
+            for (int q = 0; q < blocks; ++q) w += unit_span<TS>(p, s, q, R).count;
+    }
+    for (unsigned m = __ballot_sync(FULL_MASK, blocks > 2); m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        const KV8Seq s = kv8_seq_checked(p.x, __shfl_sync(FULL_MASK, b, src));
+        const int n = __shfl_sync(FULL_MASK, blocks, src);
+        int64_t sum = 0;
+        for (int q = lane; q < n; q += 32) sum += unit_span<TS>(p, s, q, R).count;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+        if (lane == src) w = sum;
+    }
     return w * p.Hkv;
 }
 
 struct KV8Start {
-    int64_t lo, hi, total, base;
+    int64_t lo, hi, base;
     int b, qt, hk, j0, flags;
     int64_t warp_sum[32];
 };
 
 // The CTA's part [lo, hi) of the line of all tiles (sequence, query block, key head, tile), and the
-// unit that holds lo.  Every thread of the CTA calls it.
+// unit that holds lo.  Every thread of the CTA calls it.  least: tiles a part has at least.
 template <int TS, int R, int THREADS>
-__device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st)
+__device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st, int least)
 {
     constexpr int NWARP = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int B = p.x.B;
-    int64_t sum = 0;
+    int64_t sum = 0, mine = 0;
     int bad = 0;
-    for (int b = threadIdx.x; b < B; b += THREADS) {
-        bad |= !kv8_seq(p.x, b).ok;
-        sum += seq_tiles<TS>(p, kv8_seq_checked(p.x, b), R);
+    for (int b0 = 0; b0 < B; b0 += THREADS) {
+        const int b = b0 + static_cast<int>(threadIdx.x);
+        if (b < B) bad |= !kv8_seq(p.x, b).ok;
+        mine = seq_tiles<TS>(p, b < B ? b : -1, R, lane);
+        sum += mine;
     }
-    const int64_t mine = sum;  // of the only sequence, when there are no more than threads
     bad = __syncthreads_or(bad);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
@@ -124,16 +142,14 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st)
 #pragma unroll
     for (int w = 0; w < NWARP; ++w) total += st.warp_sum[w];
     __syncthreads();
-    // parts of at least one tile a warp
-    const int64_t least = (total + NWARP - 1) / NWARP;
-    const int64_t parts = least < static_cast<int64_t>(gridDim.x) ? least : gridDim.x;
+    const int64_t most = (total + least - 1) / least;
+    const int64_t parts = most < static_cast<int64_t>(gridDim.x) ? most : gridDim.x;
     const int64_t id = blockIdx.x;
     const int64_t lo = id < parts ? total / parts * id + total % parts * id / parts : total;
     const int64_t hi = id < parts ? total / parts * (id + 1) + total % parts * (id + 1) / parts : total;
     if (threadIdx.x == 0) {
         st.lo = lo;
         st.hi = hi;
-        st.total = total;
         st.b = st.qt = st.hk = st.j0 = 0;
         st.flags = bad ? ST_CACHE_INDEX : 0;
         st.base = 0;
@@ -144,8 +160,8 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st)
     }
     int64_t base = 0;
     for (int b0 = 0; b0 < B; b0 += THREADS) {
-        const int b = b0 + threadIdx.x;
-        const int64_t w = B <= THREADS ? mine : b < B ? seq_tiles<TS>(p, kv8_seq_checked(p.x, b), R) : 0;
+        const int b = b0 + static_cast<int>(threadIdx.x);
+        const int64_t w = B <= THREADS ? mine : seq_tiles<TS>(p, b < B ? b : -1, R, lane);
         int64_t inc = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -168,19 +184,29 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st)
         __syncthreads();
         if (lo < base) break;
     }
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
         const KV8Seq s = kv8_seq_checked(p.x, st.b);
-        int64_t rem = lo - st.base;
         const int blocks = unit_blocks(p, s, R);
-        for (int q = 0; q < blocks; ++q) {
-            const int c = unit_span<TS>(p, s, q, R).count;
-            if (rem < static_cast<int64_t>(c) * p.Hkv) {
-                st.qt = q;
-                st.hk = static_cast<int>(rem / c);
-                st.j0 = static_cast<int>(rem % c);
-                break;
+        int64_t rem = lo - st.base;
+        for (int q0 = 0; q0 < blocks; q0 += 32) {
+            const int q = q0 + lane;
+            const int c = q < blocks ? unit_span<TS>(p, s, q, R).count : 0;
+            const int64_t w = static_cast<int64_t>(c) * p.Hkv;
+            int64_t inc = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(FULL_MASK, inc, o);
+                if (lane >= o) inc += y;
             }
-            rem -= static_cast<int64_t>(c) * p.Hkv;
+            if (rem >= inc - w && rem < inc) {
+                const int64_t r = rem - (inc - w);
+                st.qt = q;
+                st.hk = static_cast<int>(r / c);
+                st.j0 = static_cast<int>(r % c);
+            }
+            const int64_t all = __shfl_sync(FULL_MASK, inc, 31);
+            if (rem < all) break;
+            rem -= all;
         }
     }
     __syncthreads();
@@ -221,5 +247,12 @@ __device__ __forceinline__ void store_row(const AttnKV8Params &p, const KV8Seq &
     *reinterpret_cast<uint2 *>(p.out + row * d_h + c) = w;
     if (c == 0 && p.lse) p.lse[row] = empty ? -INFINITY : (lg2(sum) + top) * 0.6931471805599453f;
 }
+
+// Query rows a unit of the tensor-memory kernel has, and whether a call takes that kernel.
+constexpr int KV8_TC_ROWS = 256, KV8_TC_MAX_CTAS = 160;
+inline bool kv8_takes_tc(int64_t T, int B, int ratio) { return T * ratio > static_cast<int64_t>(B) * 32; }
+cudaError_t attention_kv8_tc_launch(const AttnKV8Params &p, int d_h, const DeviceInfo &dev, cudaStream_t stream);
+// Joins the partial rows that `ctas` CTAs left, R rows a unit.
+cudaError_t attention_kv8_join_launch(const AttnKV8Params &p, int d_h, int ctas, int R, cudaStream_t stream);
 
 }  // namespace qkq
