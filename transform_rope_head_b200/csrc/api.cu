@@ -682,6 +682,8 @@ int qkq_attention_kv8(const void *q, int dtype, int64_t T, const int32_t *cu_new
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.ratio = Hq / Hkv;
+    while ((1 << p.ratio_shift) < p.ratio) ++p.ratio_shift;
+    p.ratio_mul = static_cast<uint32_t>(((1ull << (31 + p.ratio_shift)) + p.ratio - 1) / p.ratio);
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     // a window as long as the longest sequence hides nothing
     p.window = window < static_cast<int64_t>(max_pages) * page_size ? window : 0;

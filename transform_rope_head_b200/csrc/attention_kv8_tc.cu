@@ -5,18 +5,24 @@
 // share every tile of 128 cached tokens.  Per tile of tokens and query tile
 //   S [128 x 128] = Q K^T            tcgen05.mma kind::f16, both operands in shared memory
 //   P = 2^(S c_j + log2 vs_j - m)    one thread per row, S read from tensor memory
-//   O [128 x d_h] += P V             tcgen05.mma with P in tensor memory, over S's own columns
-// with fp32 accumulators.  The codes become fp16 on their way to shared memory (exact), K as rows of
-// tokens, V transposed to rows of channels, both in the 128-byte swizzle.
+//   O [128 x d_h] += P V             tcgen05.mma with P in tensor memory, over S's upper columns
+// with fp32 accumulators.  The codes become fp16 on their way to shared memory (exact), rows of
+// tokens for K and V alike in the 128-byte swizzle (V is read channels-major).
 //
 // Warps: 0-3 and 4-7 one query tile each (a thread a row: no exchange for maxima or sums), 8-11
-// load and convert K and V two tiles ahead, one thread of warp 12 issues the MMAs (warps 13-15 only
-// complete its warpgroup, which gives up registers) in the order
+// load and convert K and V two tiles ahead, 13-15 scale the next unit's queries into fp16, one
+// thread of warp 12 issues the MMAs in the order
 //   S0(i) S1(i) | PV0(i) S0(i+1) PV1(i) S1(i+1) | ...
 // so that the tensor cores work on one tile while the other's exponentials are taken.
 //
+// A row's thread reads S twice, for the maximum and for the exponentials, in chunks of 32 columns
+// and rolled loops: the roles together have to fit the instruction caches (fully unrolled, their
+// warps spent more time waiting for instructions than in any pipe).
+//
 // The maximum is an integer and moves only when a logit passes it by more than 2^8, so rescaling
 // what was summed is rare, exact, and can be done to what is already stored.
+#include <limits.h>
+
 #include "attention_kv8.cuh"
 #include "tcgen05.cuh"
 
@@ -27,17 +33,23 @@ namespace {
 constexpr int TS = 128;            // cached tokens of a tile
 constexpr int TC_THREADS = 16 * 32;
 constexpr int CONV0 = 8 * 32;      // first converting thread
+constexpr int QLOAD0 = 13 * 32, QLOAD_WARPS = 3;
 constexpr int RING = 4;            // tiles whose steps are kept
+constexpr int BLOCK = 128 * 128;   // bytes of 64 channels of 128 rows
+template <int DH>
+constexpr int QBUF = DH == 64 ? 2 : 1;  // units whose queries are held: what shared memory has room for
 
 template <int DH>
 struct __align__(1024) TcSmem {
-    uint8_t q[2][DH / 64][128 * 128];
-    uint8_t k[2][DH / 64][128 * 128];
-    uint8_t v[2][2][DH * 128];
-    float ks[RING][8], lvs[RING][8], ivs[RING][8];  // per 16 tokens
+    uint8_t k[2][DH / 64][BLOCK];
+    uint8_t v[2][DH / 64][BLOCK];
+    uint8_t q[QBUF<DH>][2][DH / 64][BLOCK];
+    float4 step[RING][8];                           // per 16 tokens: key step, log2 and inverse of the value step
+    int2 tile[RING];                                // first token; whether every row sees all of the tile
+    float fac[2][256];                              // per unit and row: what a product is times to be a base-2 logit
     int nan_unit[4];                                // number + 1 of the unit whose masked tiles hold NaN values
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[QBUF<DH>][2], q_empty[QBUF<DH>][2], s_full[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
     KV8Start start;
 };
@@ -104,11 +116,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
     return __any_sync(FULL_MASK, mbar_wait_bounded(bar, parity));
 }
 
-// Registers per thread of the warpgroups, 128 at launch: 2 x 152 + 128 + 80 = 4 x 128.
+// Registers per thread of the warpgroups, 128 at launch: 2 x 136 + 128 + 112 = 4 x 128.
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Every row of a unit sees every token of the tile at tok0.
+__device__ __forceinline__ bool all_visible(const AttnKV8Params &p, const KV8Span &span, int tok0)
+{
+    return tok0 + TS - 1 <= span.first && (p.window == 0 || tok0 > span.last - p.window || tok0 + TS - 1 < p.sinks);
+}
 
 // The units of a CTA's part, each warp role on its own.
 struct Units {
@@ -136,170 +154,240 @@ struct Units {
         if (j1 == span.count && cur < hi) next_unit(p, s, KV8_TC_ROWS, b, qt, hk);
     }
     __device__ __forceinline__ int token(int j) const { return TS * (j < span.head ? j : j + span.skip); }
-    // every row of the unit sees every token of the tile at tok0
-    __device__ __forceinline__ bool full(const AttnKV8Params &p, int tok0) const
-    {
-        return tok0 + TS - 1 <= span.first && (p.window == 0 || tok0 > span.last - p.window || tok0 + TS - 1 < p.sinks);
-    }
+    __device__ __forceinline__ bool full(const AttnKV8Params &p, int tok0) const { return all_visible(p, span, tok0); }
 };
 
-// Channel ch of a Q or K row: 64-channel block and 16-byte place in it.  With 128 channels the block is
-// which half of 16 channels it is in, so that the 8 lanes that convert a row's 16-byte loads
+// Channels 8 c8 .. of a Q, K or V row: 64-channel block and 16-byte place in it.  With 128 channels the block
+// is which half of 16 channels it is, so that the 8 lanes that convert a row's 16-byte loads
 // store to 8 different places of one 128-byte line.
 template <int DH>
 __device__ __forceinline__ uint32_t row_offset(int r, int c8)
 {
     const int blk = DH == 128 ? (c8 & 1) : 0, place = DH == 128 ? (c8 >> 1) : c8;
-    return static_cast<uint32_t>(blk * 128 * 128 + r * 128 + ((place ^ (r & 7)) << 4));
+    return static_cast<uint32_t>(blk * BLOCK + r * 128 + ((place ^ (r & 7)) << 4));
+}
+
+// The channel that stands at column n (a multiple of 8) of O.
+template <int DH>
+__device__ __forceinline__ int column_channel(int n)
+{
+    return DH == 128 ? 16 * ((n >> 3) & 7) + 8 * (n >> 6) : n;
 }
 
 template <int DH>
 __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> &sm, int &flags)
 {
-    constexpr int LPR = DH / 16;       // lanes per K row
-    constexpr int KIT = LPR;           // K iterations: 128 / LPR rows each
-    constexpr int VB = DH / 8;         // V bytes per token and lane
-    constexpr int VW = VB / 4;
+    constexpr int LPR = DH / 16;       // lanes per row
+    constexpr int IT = LPR;            // rows per thread, 128 / LPR apart
     const int tid = threadIdx.x - CONV0, lane = tid & 31;
     const int kc = tid % LPR, kr = tid / LPR;
-    const int tgl = tid & 7, vc = (tid >> 3) & 7, tgh = tid >> 6;
-    const int64_t mask = (1 << p.x.page_shift) - 1;
+    const int in_slice = (kr & 15) * DH + 16 * kc;  // the thread's bytes within any 16-token slice
+    const uint32_t dst0 = row_offset<DH>(kr, 2 * kc), dst1 = row_offset<DH>(kr, 2 * kc + 1);
     int n = 0;  // tiles so far
     Units u(sm.start);
-    uint4 kw[KIT];
-    uint32_t vw[8][VW];
+    uint4 kw[IT], vw[IT];
+    float ks = 0.0f, vs = 0.0f;
+    int id = -1;            // in lanes 0-7: the page of each slice of the tile being loaded, as the table has it
+    int64_t at = 0;         // in lanes 0-7: where the slice begins in the cache's codes
+    uint32_t none = 0;      // slices without a page (nothing cached there, or a bad page)
 
-    // page of each 16-token slice of a tile, in lanes 0-7
-    auto pages = [&](int j) {
+    auto page_id = [&](int j) {
         const int tok = u.token(j) + 16 * (lane & 7);
-        if (j >= u.j1 || tok >= u.s.len) return -1;
-        const int id = kv8_page(p.x, u.b, tok >> p.x.page_shift);
-        if (id < 0) flags |= ST_CACHE_INDEX;
-        return id;
+        return j < u.j1 && tok < u.s.len ? __ldg(p.x.block_table + static_cast<int64_t>(u.b) * p.x.max_pages + (tok >> p.x.page_shift)) : -1;
     };
-    auto load_k = [&](int j, int pg) {
-        const int tok0 = u.token(j);
+    // tile j's slices, from the page ids (loaded before)
+    auto locate = [&](int j) {
+        const int tok = u.token(j) + 16 * (lane & 7);
+        const bool ok = id >= 0 && id < p.x.num_pages;
+        if (!ok && tok < u.s.len) flags |= ST_CACHE_INDEX;
+        none = __ballot_sync(FULL_MASK, !ok) & 0xffu;
+        const int64_t ph = static_cast<int64_t>(ok ? id : 0) * p.Hkv + u.hk;
+        at = ((ph << p.x.page_shift) + (tok & ((1 << p.x.page_shift) - 1))) * DH;
+        if (tid < 8) {
+            ks = __ldg(p.k_steps + ph);
+            vs = __ldg(p.v_steps + ph);
+        }
+    };
+    auto load = [&](uint4 (&w)[IT], const uint8_t *codes) {
 #pragma unroll
-        for (int i = 0; i < KIT; ++i) {
+        for (int i = 0; i < IT; ++i) {
+            const int64_t slice = __shfl_sync(FULL_MASK, at, (kr >> 4) + i * (8 / IT));
+            w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + slice + in_slice));
+        }
+    };
+    // rows of slices that `gone` names, and rows from `end` on, become zero
+    auto clear = [&](uint4 (&w)[IT], uint32_t gone, int end) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
             const int r = kr + i * (128 / LPR);
-            const int id = __shfl_sync(FULL_MASK, pg, r >> 4);
-            kw[i] = make_uint4(0, 0, 0, 0);
-            if (id >= 0) {
-                const int64_t row = ((static_cast<int64_t>(id) * p.Hkv + u.hk) << p.x.page_shift) + ((tok0 + r) & mask);
-                kw[i] = __ldg(reinterpret_cast<const uint4 *>(p.k_codes + row * DH + 16 * kc));
-            }
+            if (((gone >> (r >> 4)) & 1) || r >= end) w[i] = make_uint4(0, 0, 0, 0);
         }
     };
-    auto load_v = [&](int j, int pg) {
-        const int tok0 = u.token(j) + 64 * tgh + 8 * tgl;
-        const int id = __shfl_sync(FULL_MASK, pg, 4 * tgh + (tgl >> 1));
-        const int64_t row = ((static_cast<int64_t>(id) * p.Hkv + u.hk) << p.x.page_shift) + (tok0 & mask);
+    auto store = [&](uint8_t *dst, const uint4 (&w)[IT]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < IT; ++i) {
+            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            uint32_t h[8];
 #pragma unroll
-            for (int w = 0; w < VW; ++w) vw[i][w] = 0;
-            if (id >= 0 && tok0 + i < u.s.len) {
-                const uint8_t *src = p.v_codes + (row + i) * DH + VB * vc;
-                if (DH == 128) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
-                    vw[i][0] = x.x;
-                    vw[i][1] = x.y;
-                    vw[i][VW - 2] = x.z;
-                    vw[i][VW - 1] = x.w;
-                } else {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
-                    vw[i][0] = x.x;
-                    vw[i][1] = x.y;
-                }
+            for (int k = 0; k < 4; ++k) {
+                h[2 * k] = e4m3x2_to_half2(x[k] & 0xffffu);
+                h[2 * k + 1] = e4m3x2_to_half2(x[k] >> 16);
             }
+            *reinterpret_cast<uint4 *>(dst + dst0 + i * (128 / LPR) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(dst + dst1 + i * (128 / LPR) * 128) = make_uint4(h[4], h[5], h[6], h[7]);
         }
+        fence_proxy_async_smem();
+        __syncwarp();
     };
 
     bool more = u.open(p);
-    int pg = -1;
+    int j = u.j0;
     if (more) {
-        pg = pages(u.j0);
-        load_k(u.j0, pg);
-        load_v(u.j0, pg);
+        id = page_id(j);
+        locate(j);
+        load(kw, p.k_codes);
+        load(vw, p.v_codes);
+        id = page_id(j + 1);
     }
     while (more) {
-        for (int j = u.j0; j < u.j1; ++j, ++n) {
-            const int st = n & 1;
-            const uint32_t par = ((n >> 1) & 1) ^ 1;
-            const int tok0 = u.token(j);
-            const bool last = j + 1 == u.j1;
-            const int pg_next = last ? -1 : pages(j + 1);
-            // steps of the tile's slices
-            float ks = 0.0f, vs = 1.0f;
-            if (tid < 8 && pg >= 0) {
-                const int64_t ph = static_cast<int64_t>(pg) * p.Hkv + u.hk;
-                ks = kv8_step(p.k_steps, ph);
-                vs = kv8_step(p.v_steps, ph);
-            }
-            if (!warp_wait(smem_addr(&sm.k_empty[st]), par)) return false;
-            if (tid < 8) {
-                sm.ks[n % RING][tid] = ks;
-                sm.lvs[n % RING][tid] = pg >= 0 ? lg2(vs) : -INFINITY;
-                sm.ivs[n % RING][tid] = pg >= 0 ? 1.0f / vs : 0.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < KIT; ++i) {
-                const int r = kr + i * (128 / LPR);
-                const uint32_t x[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w};
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<uint4 *>(&sm.k[st][0][0] + row_offset<DH>(r, 2 * kc + h)) =
-                        make_uint4(e4m3x2_to_half2(x[2 * h] & 0xffffu), e4m3x2_to_half2(x[2 * h] >> 16),
-                                   e4m3x2_to_half2(x[2 * h + 1] & 0xffffu), e4m3x2_to_half2(x[2 * h + 1] >> 16));
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sm.k_full[st]));
-            if (!last) load_k(j + 1, pg_next);
-
-            if (!u.full(p, tok0)) {
-                // NaN value codes that some row must not see (0 * NaN): out of the sums; the rows that
-                // see them are looked after at the unit's end
-                uint32_t any = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int w = 0; w < VW; ++w) {
-                        const uint32_t nb = e4m3_nan_bits(vw[i][w]) >> 7;
-                        vw[i][w] &= ~(nb * 0xffu);
-                        any |= nb;
-                    }
-                if (any) *reinterpret_cast<volatile int *>(&sm.nan_unit[u.number & 3]) = u.number + 1;
-            }
-            if (!warp_wait(smem_addr(&sm.v_empty[st]), par)) return false;
-#pragma unroll
-            for (int w = 0; w < VW; ++w)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t a[4], b[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t x = __byte_perm(vw[2 * i][w], vw[2 * i + 1][w], h ? 0x7362 : 0x5140);
-                        a[i] = e4m3x2_to_half2(x & 0xffffu);
-                        b[i] = e4m3x2_to_half2(x >> 16);
-                    }
-                    const int ch = VB * vc + 4 * w + 2 * h;
-                    uint8_t *dst = &sm.v[st][tgh][0] + ch * 128;
-                    *reinterpret_cast<uint4 *>(dst + ((tgl ^ (ch & 7)) << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
-                    *reinterpret_cast<uint4 *>(dst + 128 + ((tgl ^ ((ch + 1) & 7)) << 4)) = make_uint4(b[0], b[1], b[2], b[3]);
-                }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sm.v_full[st]));
-            if (!last) load_v(j + 1, pg_next);
-            pg = pg_next;
+        const int st = n & 1;
+        const uint32_t par = ((n >> 1) & 1) ^ 1;
+        const int tok0 = u.token(j), end = u.s.len - tok0, number = u.number;
+        const bool full = u.full(p, tok0);
+        const uint32_t gone = none;
+        if (!warp_wait(smem_addr(&sm.k_empty[st]), par)) return false;
+        if (tid < 8) {
+            const bool here = !((none >> tid) & 1);
+            const float k1 = fminf(fmaxf(ks, KV8_STEP_MIN), KV8_STEP_MAX), v1 = fminf(fmaxf(vs, KV8_STEP_MIN), KV8_STEP_MAX);
+            sm.step[n % RING][tid] = make_float4(here ? k1 : 0.0f, here ? lg2(v1) : -INFINITY, here ? 1.0f / v1 : 0.0f, 0.0f);
+            if (tid == 0) sm.tile[n % RING] = make_int2(tok0, full);
         }
-        u.close(p);
-        more = u.open(p);
+        if (gone) clear(kw, gone, 128);
+        store(&sm.k[st][0][0], kw);
+        if (lane == 0) mbar_arrive(smem_addr(&sm.k_full[st]));
+        // on to the next tile, of this unit or the next one
+        if (++j == u.j1) {
+            u.close(p);
+            more = u.open(p);
+            j = u.j0;
+            if (more) id = page_id(j);
+        }
         if (more) {
-            pg = pages(u.j0);
-            load_k(u.j0, pg);
-            load_v(u.j0, pg);
+            locate(j);
+            load(kw, p.k_codes);
+            id = page_id(j + 1);
+        }
+        if (!full) {
+            clear(vw, gone, end);
+            // NaN value codes that some row must not see (0 * NaN): out of the sums; the rows that
+            // see them are looked after at the unit's end
+            uint32_t any = 0;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                uint32_t x[4] = {vw[i].x, vw[i].y, vw[i].z, vw[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t nb = e4m3_nan_bits(x[k]) >> 7;
+                    x[k] &= ~(nb * 0xffu);
+                    any |= nb;
+                }
+                vw[i] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            if (any) *reinterpret_cast<volatile int *>(&sm.nan_unit[number & 3]) = number + 1;
+        } else if (gone) {
+            clear(vw, gone, 128);
+        }
+        if (!warp_wait(smem_addr(&sm.v_empty[st]), par)) return false;
+        store(&sm.v[st][0][0], vw);
+        if (lane == 0) mbar_arrive(smem_addr(&sm.v_full[st]));
+        if (more) load(vw, p.v_codes);
+        ++n;
+    }
+    return true;
+}
+
+__device__ __forceinline__ uint32_t bf16_pair_to_half(uint32_t w, float f)
+{
+    return pack16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f, true);
+}
+
+// Queries of the units, a row on DH / 8 lanes: fp16 as they are, bf16 scaled by a power of two per row
+// into fp16's range; with the sign of the softmax scale, so that a row's factor is not negative.
+template <int DH>
+__device__ __forceinline__ bool query_role(const AttnKV8Params &p, TcSmem<DH> &sm)
+{
+    constexpr int LPR = DH / 8, RPW = 32 / LPR, STRIDE = QLOAD_WARPS * RPW, BATCH = 6;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x - QLOAD0) >> 5;
+    const int c8 = lane % LPR, first = warp * RPW + lane / LPR;
+    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    const float scale = fabsf(p.scale_log2);
+    int un[QBUF<DH>][2] = {};
+    Units u(sm.start);
+    for (; u.open(p); u.close(p)) {
+        const int buf = u.number % QBUF<DH>;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if (t * 128 >= u.rows) break;
+            const int rows = min(128, u.rows - t * 128);
+            int &turn = un[QBUF<DH> == 1 ? 0 : buf][t];
+            const int rr0 = u.qt * KV8_TC_ROWS + t * 128, token0 = p.div_ratio(rr0);
+            const uint16_t *src = p.q + (static_cast<int64_t>(u.s.q0 + token0) * p.Hq + u.hk * p.ratio + rr0 - token0 * p.ratio) * DH + 8 * c8;
+            uint8_t *dst = &sm.q[buf][t][0][0];
+            bool waited = turn == 0;
+#pragma unroll 1
+            for (int r0 = first; r0 < 128; r0 += STRIDE * BATCH) {
+                uint4 w[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int r = r0 + i * STRIDE;
+                    // at most 128 tokens of 2^16 heads on: 32 bits
+                    const uint32_t off = static_cast<uint32_t>(r + (p.div_ratio(rr0 + r) - token0) * (p.Hq - p.ratio)) * DH;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (r < rows) w[i] = __ldg(reinterpret_cast<const uint4 *>(src + off));
+                }
+                if (!waited && !warp_wait(smem_addr(&sm.q_empty[buf][t]), (turn - 1) & 1)) return false;
+                waited = true;
+                float up[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) up[i] = scale;
+                if (!p.half) {
+                    uint32_t top[BATCH];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        // non-negative bf16 pairs compare as they are in the upper half, the lower one shifted there
+                        const uint32_t a = w[i].x & 0x7fff7fffu, b = w[i].y & 0x7fff7fffu, c = w[i].z & 0x7fff7fffu, d = w[i].w & 0x7fff7fffu;
+                        top[i] = max(max(max(a, b), max(c, d)), max(max(a << 16, b << 16), max(c << 16, d << 16)));
+                    }
+#pragma unroll
+                    for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i) top[i] = max(top[i], __shfl_xor_sync(FULL_MASK, top[i], o));
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        // a row that is not finite stays so under any factor
+                        const int e = row_exponent(__uint_as_float(min(top[i] & 0xffff0000u, 0x7f7f0000u)));
+                        const float f = exp2i(-e);
+                        up[i] = scale * exp2i(e);
+                        w[i].x = bf16_pair_to_half(w[i].x, f);
+                        w[i].y = bf16_pair_to_half(w[i].y, f);
+                        w[i].z = bf16_pair_to_half(w[i].z, f);
+                        w[i].w = bf16_pair_to_half(w[i].w, f);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int r = r0 + i * STRIDE;
+                    if (r < 128) {
+                        *reinterpret_cast<uint4 *>(dst + row_offset<DH>(r, c8)) =
+                            make_uint4(w[i].x ^ flip, w[i].y ^ flip, w[i].z ^ flip, w[i].w ^ flip);
+                        if (c8 == 0) sm.fac[u.number & 1][t * 128 + r] = up[i];
+                    }
+                }
+            }
+            ++turn;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[buf][t]));
         }
     }
     return true;
@@ -308,68 +396,243 @@ __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> 
 template <int DH>
 __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm, uint32_t tmem)
 {
-    const uint32_t id_s = idesc_f16(TS), id_o = idesc_f16(DH);
-    int n = 0, cnt[2] = {0, 0}, un[2] = {0, 0};  // tiles; tiles and units of each query tile
-    auto scores = [&](int t, int st, bool last_reader) {
-        uint64_t q = sw128_desc(smem_addr(&sm.q[t][0][0])), k = sw128_desc(smem_addr(&sm.k[st][0][0]));
-        asm volatile("" : "+l"(q), "+l"(k));  // built here, not kept in registers for every step
-#pragma unroll
-        for (int s = 0; s < DH / 16; ++s) {
-            const uint32_t off = ((s >> 2) * (128 * 128) + (s & 3) * 32) >> 4;
-            mma_bf16(tmem + t * TS, q + off, k + off, id_s, s ? 1u : 0u);
-        }
-        mma_commit(smem_addr(&sm.s_full[t]));
-        if (last_reader) mma_commit(smem_addr(&sm.k_empty[st]));
-    };
-    auto values = [&](int t, int st, bool accumulate, bool last_reader) {
-        uint64_t v = sw128_desc(smem_addr(&sm.v[st][0][0]));
-        asm volatile("" : "+l"(v));
-#pragma unroll
-        for (int s = 0; s < TS / 16; ++s)
-            mma_f16_ts(tmem + 2 * TS + t * DH, tmem + t * TS + 8 * s, v + (((s >> 2) * (DH * 128) + (s & 3) * 32) >> 4), id_o,
-                       accumulate || s ? 1u : 0u);
-        mma_commit(smem_addr(&sm.o_done[t]));
-        if (last_reader) mma_commit(smem_addr(&sm.v_empty[st]));
-    };
+    const uint32_t id_s = idesc_f16(TS), id_o = idesc_f16(DH) | (1u << 16);  // V: channels-major
+    // K, Q: rows of 64 channels, 8-row groups 1024 bytes apart; V: 64 channels of a token a row, 8-token
+    // groups 1024 bytes, 64-channel blocks BLOCK bytes apart
+    const uint64_t q0 = sw128_desc(smem_addr(&sm.q[0][0][0][0])), k0 = sw128_desc(smem_addr(&sm.k[0][0][0]));
+    const uint64_t v0 = (sw128_desc(smem_addr(&sm.v[0][0][0])) & ~(0x3fffull << 16)) | (static_cast<uint64_t>(BLOCK >> 4) << 16);
+    constexpr uint64_t STAGE = (DH / 64) * (BLOCK >> 4);
+    int n = 0, cnt[2] = {0, 0}, un[QBUF<DH>][2] = {};  // tiles; tiles and units of each query tile
     Units u(sm.start);
     while (u.open(p)) {
-        const bool two = u.rows > 128;
-        for (int t = 0; t <= (two ? 1 : 0); ++t) {
-            if (!mbar_wait_bounded(smem_addr(&sm.q_full[t]), un[t] & 1)) return false;
-            ++un[t];
-            if (t == 0 && !mbar_wait_bounded(smem_addr(&sm.k_full[n & 1]), (n >> 1) & 1)) return false;
-            tc_fence_after();
-            scores(t, n & 1, t == (two ? 1 : 0));
-        }
-        for (int j = u.j0; j < u.j1; ++j, ++n) {
-            const bool more = j + 1 < u.j1;
-            const int st = n & 1, next = (n + 1) & 1;
-            if (!mbar_wait_bounded(smem_addr(&sm.v_full[st]), (n >> 1) & 1)) return false;
-            for (int t = 0; t <= (two ? 1 : 0); ++t) {
-                const bool last = t == (two ? 1 : 0);
-                if (!mbar_wait_bounded(smem_addr(&sm.p_full[t]), cnt[t] & 1)) return false;
-                ++cnt[t];
-                tc_fence_after();
-                values(t, st, j > u.j0, last);
-                if (more) {
-                    if (t == 0 && !mbar_wait_bounded(smem_addr(&sm.k_full[next]), ((n + 1) >> 1) & 1)) return false;
+        const int last_t = u.rows > 128 ? 1 : 0, buf = u.number % QBUF<DH>;
+#pragma unroll 1
+        for (int j = u.j0; j <= u.j1; ++j, ++n) {
+            // tile j - 1's values, then tile j's scores (which take the columns that P leaves)
+            const int st = n & 1;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (t > last_t) break;
+                if (j > u.j0) {
+                    if (t == 0 && !mbar_wait_bounded(smem_addr(&sm.v_full[st ^ 1]), ((n - 1) >> 1) & 1)) return false;
+                    if (!mbar_wait_bounded(smem_addr(&sm.p_full[t]), cnt[t] & 1)) return false;
+                    ++cnt[t];
                     tc_fence_after();
-                    scores(t, next, last);
+                    const uint64_t v = v0 + (st ^ 1) * STAGE;
+#pragma unroll
+                    for (int s = 0; s < TS / 16; ++s)
+                        mma_f16_ts(tmem + 2 * TS + t * DH, tmem + t * TS + TS / 2 + 8 * s, v + s * (16 * 128 >> 4), id_o,
+                                   s || j - 1 > u.j0 ? 1u : 0u);
+                    if (t == last_t) mma_commit(smem_addr(&sm.v_empty[st ^ 1]));
+                    if (j == u.j1) mma_commit(smem_addr(&sm.o_done[t]));
+                } else {
+                    int &turn = un[QBUF<DH> == 1 ? 0 : buf][t];
+                    if (!mbar_wait_bounded(smem_addr(&sm.q_full[buf][t]), turn & 1)) return false;
+                    ++turn;
+                }
+                if (j < u.j1) {
+                    if (t == 0 && !mbar_wait_bounded(smem_addr(&sm.k_full[st]), (n >> 1) & 1)) return false;
+                    tc_fence_after();
+                    const uint64_t q = q0 + (2 * buf + t) * STAGE, k = k0 + st * STAGE;
+#pragma unroll
+                    for (int s = 0; s < DH / 16; ++s) {
+                        const uint32_t off = ((s >> 2) * BLOCK + (s & 3) * 32) >> 4;
+                        mma_bf16(tmem + t * TS, q + off, k + off, id_s, s ? 1u : 0u);
+                    }
+                    // done when all before it is, the last tile's values among that
+                    mma_commit(smem_addr(&sm.s_full[t]));
+                    if (t == last_t) mma_commit(smem_addr(&sm.k_empty[st]));
+                    if (j + 1 == u.j1) mma_commit(smem_addr(&sm.q_empty[buf][t]));
                 }
             }
         }
+        --n;
         u.close(p);
     }
     return true;
 }
 
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Which columns of a tile the row sees: those below hi, and not in [lo, ...) unless below sk.
+struct RowMask {
+    int hi, lo, sk;
+    static __device__ __forceinline__ uint32_t below(int n)
+    {
+        return n >= 32 ? FULL_MASK : (1u << max(n, 0)) - 1u;
+    }
+    // bits of columns c0 .. c0 + 31
+    __device__ __forceinline__ uint32_t bits(int c0) const { return below(hi - c0) & (~below(lo - c0) | below(sk - c0)); }
+};
+
+// The largest base-2 logit (without the maximum's offset) of 32 columns.
+template <bool MASKED>
+__device__ __forceinline__ float chunk_top(const uint32_t (&raw)[32], const float4 *step, float fac, uint32_t bits)
+{
+    float top = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            x[i] = __uint_as_float(raw[16 * g + i]);
+            if (MASKED && !((bits >> (16 * g + i)) & 1)) x[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 1; i < 16; ++i) x[0] = fmaxf(x[0], x[i]);
+        // the factor is not negative and rounding keeps order: the logit of the maximum
+        top = fmaxf(top, __fmaf_rn(x[0], fac * step[g].x, step[g].y));
+    }
+    return top;
+}
+
+// P of 32 columns as fp16 pairs, and their part of the row's sum.
+template <bool MASKED>
+__device__ __forceinline__ void chunk_p(const uint32_t (&raw)[32], const float4 *step, float fac, float m, uint32_t bits,
+                                        uint32_t (&pw)[16], float &l)
+{
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        const float f = fac * step[g].x, a = step[g].y - m;
+        const uint64_t f2 = pair(f, f), a2 = pair(a, a);
+        uint64_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int k = 16 * g + 2 * i;
+            float x, y;
+            unpair(fma_pair(pair(__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])), f2, a2), x, y);
+            x = ex2(x);
+            y = ex2(y);
+            if (MASKED) {
+                x = (bits >> k) & 1 ? x : 0.0f;
+                y = (bits >> (k + 1)) & 1 ? y : 0.0f;
+            }
+            sum = add_pair(sum, pair(x, y));
+            pw[8 * g + i] = pack16(x, y, true);
+        }
+        float x, y;
+        unpair(sum, x, y);
+        l = __fmaf_rn(x + y, step[g].z, l);
+    }
+}
+
+// A row's statistics: m the (whole-numbered) maximum's offset, l the sum, pass what a logit must
+// exceed to move m (-inf: none seen yet).
+struct RowState {
+    float m, l, pass;
+};
+
+// S of one tile to P, the row's thread.
+template <int DH, bool MASKED>
+__device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_full, bool first, uint32_t s_cols, uint32_t o_cols,
+                                             float fac, const RowMask &mask, RowState &r)
+{
+    uint32_t a[32], b[32], pw[16];
+    tmem_ld32_async(s_cols, a);
+    tmem_ld32_async(s_cols + 32, b);
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+        tmem_ld_wait(a);
+        tmem_ld_wait(b);
+        top = fmaxf(top, chunk_top<MASKED>(a, step + 4 * h, fac, MASKED ? mask.bits(64 * h) : 0u));
+        if (h == 0) tmem_ld32_async(s_cols + 64, a);
+        top = fmaxf(top, chunk_top<MASKED>(b, step + 4 * h + 2, fac, MASKED ? mask.bits(64 * h + 32) : 0u));
+        if (h == 0) tmem_ld32_async(s_cols + 96, b);
+    }
+    const bool moves = top > r.pass;
+    if (__any_sync(FULL_MASK, moves)) {
+        // the maximum moves: a whole number, so that every factor is a power of two (before a row's
+        // first logit there is nothing to rescale)
+        const float to = moves ? ceilf(top) : r.m;
+        const float alpha = moves && r.pass > -INFINITY ? ex2(r.m - to) : 1.0f;
+        if (moves) {
+            r.m = to;
+            r.pass = to + 8.0f;
+        }
+        r.l *= alpha;
+        if (!first) {
+            // the product before this tile's S has been added to O
+#pragma unroll 1
+            for (int k = 0; k < DH / 16; ++k) {
+                uint32_t w[16];
+                tmem_ld16(o_cols + 16 * k, w);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+                tmem_st16(o_cols + 16 * k, w);
+            }
+        }
+    }
+    // backwards: the last two chunks are at hand, and P takes the upper columns once they are read
+#pragma unroll 1
+    for (int h = 1; h >= 0; --h) {
+        if (h == 0) {
+            tmem_ld_wait(a);
+            tmem_ld_wait(b);
+        }
+        chunk_p<MASKED>(b, step + 4 * h + 2, fac, r.m, MASKED ? mask.bits(64 * h + 32) : 0u, pw, r.l);
+        if (h == 1) tmem_ld32_async(s_cols + 32, b);
+        tmem_st16(s_cols + TS / 2 + 32 * h + 16, pw);
+        chunk_p<MASKED>(a, step + 4 * h, fac, r.m, MASKED ? mask.bits(64 * h) : 0u, pw, r.l);
+        if (h == 1) tmem_ld32_async(s_cols, a);
+        tmem_st16(s_cols + TS / 2 + 32 * h, pw);
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(p_full);
+}
+
+// Which of the 8 channels from ch on have a NaN value code that a row at index `at` sees in tiles
+// [j0, j1) of a unit that not every row sees wholly (the converting warps took those codes out).
+template <int DH>
+__device__ __noinline__ uint32_t nan_channels(const AttnKV8Params &p, int b, int hk, int j0, int j1, KV8Span span, int at, int ch)
+{
+    uint32_t m = 0;
+    for (int j = j0; j < j1; ++j) {
+        const int tok0 = TS * (j < span.head ? j : j + span.skip);
+        if (all_visible(p, span, tok0)) continue;
+        for (int tok = tok0; tok < tok0 + TS && tok <= at; ++tok) {
+            if (p.window && tok <= at - p.window && tok >= p.sinks) continue;
+            const int id = kv8_page(p.x, b, tok >> p.x.page_shift);
+            if (id < 0) continue;
+            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(
+                p.v_codes + (((static_cast<int64_t>(id) * p.Hkv + hk) << p.x.page_shift) + (tok & ((1 << p.x.page_shift) - 1))) * DH + ch));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m |= ((w.x >> (8 * i)) & 0x7f) == 0x7f ? 1u << i : 0u;
+                m |= ((w.y >> (8 * i)) & 0x7f) == 0x7f ? 16u << i : 0u;
+            }
+        }
+    }
+    return m;
+}
+
 template <int DH>
 __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> &sm, uint32_t tmem, const KV8Partials &part)
 {
-    const int t = threadIdx.x >> 7, r = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const int t = threadIdx.x >> 7, r = threadIdx.x & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(r & 96) << 16);
     const uint32_t s_cols = lanes + t * TS, o_cols = lanes + 2 * TS + t * DH;
-    int n = 0, cnt = 0;
+    int n = 0, cnt = 0, unit = 0;  // tiles of the part; tiles and units of this query tile
     Units u(sm.start);
     for (; u.open(p); u.close(p)) {
         if (t * 128 >= u.rows) {
@@ -379,194 +642,78 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
         const int row = t * 128 + r;
         const bool live = row < u.rows;
         const int rr = u.qt * KV8_TC_ROWS + row;
-        // ---- the row's query, scaled into fp16 -----------------------------------------------
-        float fac;
-        {
-            uint32_t w[DH / 2];
-            float amax = 0.0f;
-            if (live) {
-                const uint16_t *src = p.q + (static_cast<int64_t>(u.s.q0 + rr / p.ratio) * p.Hq + u.hk * p.ratio + rr % p.ratio) * DH;
-#pragma unroll
-                for (int i = 0; i < DH / 8; ++i) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src) + i);
-                    w[4 * i] = x.x;
-                    w[4 * i + 1] = x.y;
-                    w[4 * i + 2] = x.z;
-                    w[4 * i + 3] = x.w;
-                }
-#pragma unroll
-                for (int i = 0; i < DH / 2; ++i) {
-                    const float2 v = unpack16(w[i], p.half);
-                    amax = fmaxf(amax, fabsf(v.x) <= 3.402823466e38f ? fabsf(v.x) : 0.0f);
-                    amax = fmaxf(amax, fabsf(v.y) <= 3.402823466e38f ? fabsf(v.y) : 0.0f);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < DH / 2; ++i) w[i] = 0;
-            }
-            const int e = row_exponent(amax);
-            const float up = exp2i(-e);
-            fac = p.scale_log2 * exp2i(e);
-#pragma unroll
-            for (int i = 0; i < DH / 8; ++i) {
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 v = unpack16(w[4 * i + k], p.half);
-                    h[k] = pack16(v.x * up, v.y * up, true);
-                }
-                *reinterpret_cast<uint4 *>(&sm.q[t][0][0] + row_offset<DH>(r, i)) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[t]));
-        }
-        const int at = live ? u.s.len - u.s.n + rr / p.ratio : -1;
-        float m = 0.0f, l = 0.0f, pass = -INFINITY;  // pass: what a logit must exceed to move m (-inf: none seen yet)
-
+        const int token = p.div_ratio(rr), at = live ? u.s.len - u.s.n + token : -1;
+        RowState st{0.0f, 0.0f, -INFINITY};
+        float fac = 0.0f;
+#pragma unroll 1
         for (int j = u.j0; j < u.j1; ++j, ++n, ++cnt) {
-            const int tok0 = u.token(j);
-            const bool full = u.full(p, tok0);
-            // columns that the row sees: c <= hi and (c > lo or c < sk)
-            const int hi = at - tok0, lo = p.window ? hi - p.window : -1, sk = p.sinks - tok0;
             if (!warp_wait(smem_addr(&sm.s_full[t]), cnt & 1)) return false;
             tc_fence_after();
-            uint32_t buf[2][32];
-            tmem_ld32_async(s_cols, buf[0]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t(&raw)[32] = buf[c & 1];
-                tmem_ld_wait(raw);
-                if (c < 3) tmem_ld32_async(s_cols + 32 * (c + 1), buf[(c + 1) & 1]);
-                float x[32];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float f = fac * sm.ks[n % RING][2 * c + g], a = sm.lvs[n % RING][2 * c + g] - m;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[16 * g + i] = __fmaf_rn(__uint_as_float(raw[16 * g + i]), f, a);
-                }
-                if (!full) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int col = 32 * c + i;
-                        if (!(col <= hi && (col > lo || col < sk))) x[i] = -INFINITY;
-                    }
-                }
-                float top = x[0];
-#pragma unroll
-                for (int i = 1; i < 32; ++i) top = fmaxf(top, x[i]);
-                if (__any_sync(FULL_MASK, top > pass)) {
-                    // the maximum moves: a whole number, so that every factor is a power of two
-                    // (before a row's first logit there is nothing to rescale)
-                    const float shift = top > pass ? ceilf(top) : 0.0f;
-                    const float alpha = top > pass && pass > 0.0f ? ex2(-shift) : 1.0f;
-                    if (top > pass) {
-                        m += shift;
-                        pass = 8.0f;
-                    }
-                    l *= alpha;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] -= shift;
-                    if (c > 0) {
-                        const __half2 a2 = __float2half2_rn(alpha);
-                        if (c < 3) tmem_ld_wait(buf[(c + 1) & 1]);
-                        tmem_st_wait();
-                        for (int k = 0; k < c; ++k) {
-                            uint32_t w[16];
-                            tmem_ld16(s_cols + 16 * k, w);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&w[i]), a2);
-                                w[i] = *reinterpret_cast<const uint32_t *>(&v);
-                            }
-                            tmem_st16(s_cols + 16 * k, w);
-                        }
-                    }
-                    if (j > u.j0) {
-                        if (!warp_wait(smem_addr(&sm.o_done[t]), (cnt - 1) & 1)) return false;
-                        tc_fence_after();
-                        for (int k = 0; k < DH / 16; ++k) {
-                            uint32_t w[16];
-                            tmem_ld16(o_cols + 16 * k, w);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-                            tmem_st16(o_cols + 16 * k, w);
-                        }
-                    }
-                }
-                uint32_t pw[16];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float a = ex2(x[16 * g + 2 * i]), b = ex2(x[16 * g + 2 * i + 1]);
-                        sum += a + b;
-                        pw[8 * g + i] = pack16(a, b, true);
-                    }
-                    l = __fmaf_rn(sum, sm.ivs[n % RING][2 * c + g], l);
-                }
-                tmem_st16(s_cols + 16 * c, pw);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sm.p_full[t]));
+            const bool first = j == u.j0;
+            if (first) fac = sm.fac[u.number & 1][row];
+            const int2 tile = sm.tile[n % RING];
+            const int hi = at - tile.x + 1;
+            const RowMask mask{hi, p.window ? hi - p.window : 0, p.window ? p.sinks - tile.x : 0};
+            const uint32_t p_full = smem_addr(&sm.p_full[t]);
+            if (tile.y)
+                softmax_tile<DH, false>(sm.step[n % RING], p_full, first, s_cols, o_cols, fac, mask, st);
+            else
+                softmax_tile<DH, true>(sm.step[n % RING], p_full, first, s_cols, o_cols, fac, mask, st);
         }
 
         // ---- the unit's end ------------------------------------------------------------------------
-        if (!warp_wait(smem_addr(&sm.o_done[t]), (cnt - 1) & 1)) return false;
+        if (!warp_wait(smem_addr(&sm.o_done[t]), unit & 1)) return false;
+        ++unit;
         tc_fence_after();
         const bool whole = u.j0 == 0 && u.j1 == u.span.count;
         const bool nan = *reinterpret_cast<volatile int *>(&sm.nan_unit[u.number & 3]) == u.number + 1;
-        const float top = pass == -INFINITY ? -INFINITY : m;
+        const bool empty = st.pass == -INFINITY && st.l == 0.0f;
+        const float top = st.pass == -INFINITY ? -INFINITY : st.m;
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u.number == 0 ? 0 : 1);
-        for (int c = 0; c < DH / 32; ++c) {
+        const int64_t q_row = static_cast<int64_t>(u.s.q0) * p.Hq + u.hk * p.ratio + rr + static_cast<int64_t>(token) * (p.Hq - p.ratio);
+        const float inv = empty ? 0.0f : 1.0f / st.l;
+#pragma unroll 1
+        for (int c = 0; c < DH; c += 32) {
             uint32_t raw[32];
-            tmem_ld32_async(o_cols + 32 * c, raw);
+            tmem_ld32_async(o_cols + c, raw);
             tmem_ld_wait(raw);
-            if (nan && live) {
-                for (int j = u.j0; j < u.j1; ++j) {
-                    const int tok0 = u.token(j);
-                    if (u.full(p, tok0)) continue;
-                    for (int k = 0; k < TS && tok0 + k <= at; ++k) {
-                        const int tok = tok0 + k;
-                        if (p.window && tok <= at - p.window && tok >= p.sinks) continue;
-                        const int id = kv8_page(p.x, u.b, tok >> p.x.page_shift);
-                        if (id < 0) continue;
-                        const uint8_t *src = p.v_codes + (((static_cast<int64_t>(id) * p.Hkv + u.hk) << p.x.page_shift) + (tok & ((1 << p.x.page_shift) - 1))) * DH + 32 * c;
+            if (!live) continue;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if ((__ldg(src + i) & 0x7f) == 0x7f) raw[i] = 0x7fc00000u;
-                    }
+            for (int g = 0; g < 4; ++g) {
+                const int ch = column_channel<DH>(c + 8 * g);
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(raw[8 * g + i]);
+                if (nan) {
+                    const uint32_t bad = nan_channels<DH>(p, u.b, u.hk, u.j0, u.j1, u.span, at, ch);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = (bad >> i) & 1 ? __uint_as_float(0x7fc00000u) : o[i];
                 }
-            }
-            if (live) {
+                if (whole) {
+                    uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 v = make_float4(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1]),
-                                                 __uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3]));
-                    const int ch = 32 * c + 4 * i;
-                    if (whole) {
-                        store_row(p, u.s, rr, u.hk, ch, DH, v, top, l);
-                    } else {
-                        *reinterpret_cast<float4 *>(part.o + (slot * KV8_TC_ROWS + row) * DH + ch) = v;
-                        if (ch == 0) *reinterpret_cast<float2 *>(part.ml + (slot * KV8_TC_ROWS + row) * 2) = make_float2(top, l);
-                    }
+                    for (int i = 0; i < 4; ++i) w[i] = empty ? 0u : pack16(o[2 * i] * inv, o[2 * i + 1] * inv, p.half);
+                    *reinterpret_cast<uint4 *>(p.out + q_row * DH + ch) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(part.o + (slot * KV8_TC_ROWS + row) * DH + ch);
+                    dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                    dst[1] = make_float4(o[4], o[5], o[6], o[7]);
                 }
             }
         }
+        if (live && whole && p.lse) p.lse[q_row] = empty ? -INFINITY : (lg2(st.l) + top) * 0.6931471805599453f;
+        if (live && !whole) *reinterpret_cast<float2 *>(part.ml + (slot * KV8_TC_ROWS + row) * 2) = make_float2(top, st.l);
         tc_fence_before();
     }
     return true;
 }
 
 template <int DH>
-__global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const AttnKV8Params p)
+__global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid_constant__ AttnKV8Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     TcSmem<DH> &sm = *reinterpret_cast<TcSmem<DH> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     wait_prior_grid();
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -575,7 +722,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const AttnKV
             mbar_init(smem_addr(&sm.v_full[i]), 4);
             mbar_init(smem_addr(&sm.k_empty[i]), 1);
             mbar_init(smem_addr(&sm.v_empty[i]), 1);
-            mbar_init(smem_addr(&sm.q_full[i]), 4);
+#pragma unroll
+            for (int b = 0; b < QBUF<DH>; ++b) {
+                mbar_init(smem_addr(&sm.q_full[b][i]), QLOAD_WARPS);
+                mbar_init(smem_addr(&sm.q_empty[b][i]), 1);
+            }
             mbar_init(smem_addr(&sm.s_full[i]), 1);
             mbar_init(smem_addr(&sm.p_full[i]), 4);
             mbar_init(smem_addr(&sm.o_done[i]), 1);
@@ -602,14 +753,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const AttnKV
     int flags = threadIdx.x == 0 ? sm.start.flags : 0;
     bool ok = true;
     if (warp < 8) {
-        more_registers<152>();
+        more_registers<136>();
         ok = softmax_role<DH>(p, sm, tmem, part);
     } else if (warp < 12) {
         fewer_registers<128>();
         ok = convert_role<DH>(p, sm, flags);
     } else {
-        fewer_registers<80>();
-        if (threadIdx.x == 12 * 32) {
+        fewer_registers<112>();
+        if (warp > 12) {
+            ok = query_role<DH>(p, sm);
+        } else if (lane == 0) {
             ok = mma_role<DH>(p, sm, tmem);
             // nothing of this CTA runs on when its tensor memory goes
             mma_commit(smem_addr(&sm.drain));

@@ -238,12 +238,21 @@ struct AttnKV8Params {
     const uint8_t *k_codes, *v_codes;
     const float *k_steps, *v_steps;
     int Hq, Hkv, ratio;
+    uint32_t ratio_mul;         // ceil(2^(31 + ratio_shift) / ratio), 2^ratio_shift >= ratio
+    int ratio_shift;
     float scale_log2;           // softmax scale * log2(e)
     int window, sinks;          // window 0: none
     uint16_t *out;              // [T][Hq][d_h]
     float *lse;                 // [T][Hq], nullable
     void *workspace;
     int *status;                // nullable
+#ifdef __CUDACC__
+    // n / ratio for 0 <= n < 2^31: the multiplier is off by less than 2^ratio_shift / ratio / 2^(31 + ratio_shift)
+    __device__ __forceinline__ int div_ratio(int n) const
+    {
+        return static_cast<int>(__umulhi(static_cast<uint32_t>(n) << 1, ratio_mul) >> ratio_shift);
+    }
+#endif
 };
 
 size_t attention_kv8_workspace(int64_t T, int B, int Hq, int Hkv, int d_h);
