@@ -45,6 +45,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return r;
 }
 
+#ifndef EXTRA_S
+#define EXTRA_S 4
+#endif
+constexpr int EXTRA = EXTRA_S;  // what a unit costs besides its slices, in slices
+
 // One slice's codes and steps as this lane holds them.
 template <int DH>
 struct Slice {
@@ -109,19 +114,19 @@ __global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p
     const KV8Index &x = p.x;
     const KV8Partials part(p.workspace, gridDim.x, R, DH);
 
-    find_start<16, R, NW * 32>(p, s_start, NW);  // at least a slice per warp
-    int64_t cur = s_start.lo;
+    find_start<16, R, NW * 32>(p, s_start, EXTRA, NW);  // at least a slice per warp
+    int64_t u0 = s_start.u0;
     const int64_t hi = s_start.hi;
     int b = s_start.b, qt = s_start.qt, hk = s_start.hk;
     int j0 = s_start.j0;
-    if (threadIdx.x == 0) part.meta[blockIdx.x] = KV8Meta{cur, hi > cur ? j0 : 0, b, qt, hk};
+    if (threadIdx.x == 0) part.meta[blockIdx.x] = KV8Meta{u0, j0, b, qt, hk};
     int flags = s_start.flags;
     bool first = true;
 
-    while (cur < hi) {
+    while (u0 + EXTRA + j0 < hi) {
         const KV8Seq s = kv8_seq_checked(x, b);
         const KV8Span span = unit_span<16>(p, s, qt, R);
-        const int j1 = static_cast<int>(min(static_cast<int64_t>(span.count), j0 + (hi - cur)));
+        const int j1 = static_cast<int>(min(static_cast<int64_t>(span.count), hi - u0 - EXTRA));
         const int rows = min(R, s.n * p.ratio - qt * R);
 
         // ---- this unit's queries: B fragments, scaled per row into fp16 --------------------
@@ -370,10 +375,11 @@ __global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p
                 if (c == 0) *reinterpret_cast<float2 *>(part.ml + (slot * R + row) * 2) = make_float2(top, sum);
             }
         }
-        cur += j1 - j0;
         first = false;
+        if (j1 < span.count) break;
+        u0 += EXTRA + span.count;
         j0 = 0;
-        if (j1 == span.count && cur < hi) next_unit(p, s, R, b, qt, hk);
+        if (u0 + EXTRA < hi) next_unit(p, s, R, b, qt, hk);
     }
     if (p.status) {
         flags = __reduce_or_sync(FULL_MASK, flags);
@@ -394,19 +400,18 @@ __global__ void __launch_bounds__(256) k_attention_kv8_join(const AttnKV8Params 
     const int i = blockIdx.x + 1;
     const KV8Meta me = part.meta[i];
     if (me.j0 == 0) return;
-    const int64_t u0 = me.lo - me.j0;
     const KV8Meta prev = part.meta[i - 1];
-    if (prev.lo > u0) return;
+    if (prev.j0 > 0 && prev.u0 == me.u0) return;
     const KV8Seq s = kv8_seq_checked(p.x, me.b);
     const int row = blockIdx.y;
     if (me.qt * R + row >= s.n * p.ratio) return;
     int count = 2;  // CTA i - 1, i, and those that go on with the unit
     while (i - 1 + count < ctas) {
         const KV8Meta c = part.meta[i - 1 + count];
-        if (c.j0 == 0 || c.lo - c.j0 != u0) break;
+        if (c.j0 == 0 || c.u0 != me.u0) break;
         ++count;
     }
-    auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(i - 1) + (prev.lo == u0 ? 0 : 1) : 2 * static_cast<int64_t>(i - 1 + k); };
+    auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(i - 1) + (prev.u0 == me.u0 ? 0 : 1) : 2 * static_cast<int64_t>(i - 1 + k); };
     float top = -INFINITY;
     for (int k = threadIdx.x; k < count; k += 256) top = fmaxf(top, part.ml[(slot(k) * R + row) * 2]);
     s_m[threadIdx.x] = top;
@@ -459,18 +464,17 @@ __global__ void __launch_bounds__(256) k_attention_kv8_join_rows(const AttnKV8Pa
     const int i = blockIdx.x + 1;
     const KV8Meta me = part.meta[i];
     if (me.j0 == 0) return;
-    const int64_t u0 = me.lo - me.j0;
     const KV8Meta prev = part.meta[i - 1];
-    if (prev.lo > u0) return;
+    if (prev.j0 > 0 && prev.u0 == me.u0) return;
     const KV8Seq s = kv8_seq_checked(p.x, me.b);
     const int rows = min(R, s.n * p.ratio - me.qt * R);
     int count = 2;
     while (i - 1 + count < ctas) {
         const KV8Meta c = part.meta[i - 1 + count];
-        if (c.j0 == 0 || c.lo - c.j0 != u0) break;
+        if (c.j0 == 0 || c.u0 != me.u0) break;
         ++count;
     }
-    auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(i - 1) + (prev.lo == u0 ? 0 : 1) : 2 * static_cast<int64_t>(i - 1 + k); };
+    auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(i - 1) + (prev.u0 == me.u0 ? 0 : 1) : 2 * static_cast<int64_t>(i - 1 + k); };
     constexpr int G = 256 / (DH / 4);
     const int c = 4 * (threadIdx.x % (DH / 4));
     for (int row = blockIdx.y * G + threadIdx.x / (DH / 4); row < rows; row += gridDim.y * G) {

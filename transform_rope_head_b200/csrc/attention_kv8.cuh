@@ -10,9 +10,10 @@ namespace qkq {
 
 constexpr int KV8_MAX_CTAS = 512;  // above the persistent grids here (148 SMs x 3)
 
-// Where a CTA's part begins: its first unit continues at tile j0 of (b, qt, hk).
+// Where a CTA's part begins: with tile j0 of (b, qt, hk), the unit at place u0 of the line (j0 = 0 where the
+// part is empty).
 struct KV8Meta {
-    int64_t lo;
+    int64_t u0;
     int j0, b, qt, hk;
 };
 
@@ -88,7 +89,7 @@ __device__ __forceinline__ int unit_blocks(const AttnKV8Params &p, const KV8Seq 
 // Tiles of a sequence over all its query blocks and key heads; each lane of the warp asks for its own
 // (b < 0: none).  Long lists of blocks are summed by the whole warp.
 template <int TS>
-__device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, int b, int R, int lane)
+__device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, int b, int R, int extra, int lane)
 {
     int64_t w = 0;
     int blocks = 0;
@@ -96,14 +97,14 @@ __device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, int b, int 
         const KV8Seq s = kv8_seq_checked(p.x, b);
         blocks = unit_blocks(p, s, R);
         if (blocks <= 2)
-            for (int q = 0; q < blocks; ++q) w += unit_span<TS>(p, s, q, R).count;
+            for (int q = 0; q < blocks; ++q) w += unit_span<TS>(p, s, q, R).count + extra;
     }
     for (unsigned m = __ballot_sync(FULL_MASK, blocks > 2); m; m &= m - 1) {
         const int src = __ffs(m) - 1;
         const KV8Seq s = kv8_seq_checked(p.x, __shfl_sync(FULL_MASK, b, src));
         const int n = __shfl_sync(FULL_MASK, blocks, src);
         int64_t sum = 0;
-        for (int q = lane; q < n; q += 32) sum += unit_span<TS>(p, s, q, R).count;
+        for (int q = lane; q < n; q += 32) sum += unit_span<TS>(p, s, q, R).count + extra;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
         if (lane == src) w = sum;
@@ -112,15 +113,17 @@ __device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, int b, int 
 }
 
 struct KV8Start {
-    int64_t lo, hi, base;
+    int64_t lo, hi, base, u0;
     int b, qt, hk, j0, flags;
     int64_t warp_sum[32];
 };
 
-// The CTA's part [lo, hi) of the line of all tiles (sequence, query block, key head, tile), and the
-// unit that holds lo.  Every thread of the CTA calls it.  least: tiles a part has at least.
+// The CTA's part [lo, hi) of the line of all tiles (sequence, query block, key head, tile), on which a unit has
+// `extra` places before its tiles' (what beginning and ending it costs, in tiles), and the unit that holds lo:
+// it begins at place u0, the part with its tile j0.  Every thread of the CTA calls it.  least: places a part
+// has at least.
 template <int TS, int R, int THREADS>
-__device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st, int least)
+__device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st, int extra, int least)
 {
     constexpr int NWARP = THREADS / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -130,7 +133,7 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
     for (int b0 = 0; b0 < B; b0 += THREADS) {
         const int b = b0 + static_cast<int>(threadIdx.x);
         if (b < B) bad |= !kv8_seq(p.x, b).ok;
-        mine = seq_tiles<TS>(p, b < B ? b : -1, R, lane);
+        mine = seq_tiles<TS>(p, b < B ? b : -1, R, extra, lane);
         sum += mine;
     }
     bad = __syncthreads_or(bad);
@@ -153,6 +156,7 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
         st.b = st.qt = st.hk = st.j0 = 0;
         st.flags = bad ? ST_CACHE_INDEX : 0;
         st.base = 0;
+        st.u0 = lo;
     }
     if (lo >= hi) {
         __syncthreads();
@@ -161,7 +165,7 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
     int64_t base = 0;
     for (int b0 = 0; b0 < B; b0 += THREADS) {
         const int b = b0 + static_cast<int>(threadIdx.x);
-        const int64_t w = B <= THREADS ? mine : seq_tiles<TS>(p, b < B ? b : -1, R, lane);
+        const int64_t w = B <= THREADS ? mine : seq_tiles<TS>(p, b < B ? b : -1, R, extra, lane);
         int64_t inc = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -190,7 +194,7 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
         int64_t rem = lo - st.base;
         for (int q0 = 0; q0 < blocks; q0 += 32) {
             const int q = q0 + lane;
-            const int c = q < blocks ? unit_span<TS>(p, s, q, R).count : 0;
+            const int c = q < blocks ? unit_span<TS>(p, s, q, R).count + extra : 0;
             const int64_t w = static_cast<int64_t>(c) * p.Hkv;
             int64_t inc = w;
 #pragma unroll
@@ -202,7 +206,8 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
                 const int64_t r = rem - (inc - w);
                 st.qt = q;
                 st.hk = static_cast<int>(r / c);
-                st.j0 = static_cast<int>(r % c);
+                st.j0 = max(static_cast<int>(r % c) - extra, 0);
+                st.u0 = lo - r % c;
             }
             const int64_t all = __shfl_sync(FULL_MASK, inc, 31);
             if (rem < all) break;

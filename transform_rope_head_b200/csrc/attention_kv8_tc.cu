@@ -10,10 +10,9 @@
 // tokens for K and V alike in the 128-byte swizzle (V is read channels-major).
 //
 // Warps: 0-3 and 4-7 one query tile each (a thread a row: no exchange for maxima or sums), 8-11
-// load and convert K and V two tiles ahead, 13-15 scale the next unit's queries into fp16, one
-// thread of warp 12 issues the MMAs in the order
-//   S0(i) S1(i) | PV0(i) S0(i+1) PV1(i) S1(i+1) | ...
-// so that the tensor cores work on one tile while the other's exponentials are taken.
+// load and convert K and V two tiles ahead, 12 and 13 issue a query tile's MMAs each, S(i) | PV(i) S(i+1) | ...,
+// so that the tensor cores work on one query tile while the other's exponentials are taken, 14 and 15
+// fetch the next unit's queries.
 //
 // A row's thread reads S twice, for the maximum and for the exponentials, in chunks of 32 columns
 // and rolled loops: the roles together have to fit the instruction caches (fully unrolled, their
@@ -21,8 +20,6 @@
 //
 // The maximum is an integer and moves only when a logit passes it by more than 2^8, so rescaling
 // what was summed is rare, exact, and can be done to what is already stored.
-#include <limits.h>
-
 #include "attention_kv8.cuh"
 #include "tcgen05.cuh"
 
@@ -33,25 +30,98 @@ namespace {
 constexpr int TS = 128;            // cached tokens of a tile
 constexpr int TC_THREADS = 16 * 32;
 constexpr int CONV0 = 8 * 32;      // first converting thread
-constexpr int QLOAD0 = 13 * 32, QLOAD_WARPS = 3;
+constexpr int MMA_WARP = 12;
+constexpr int QUERY_WARP = 14;
+#ifndef EXTRA_T
+#define EXTRA_T 3
+#endif
+constexpr int EXTRA = EXTRA_T;     // what a unit costs besides its tiles, in tiles
 constexpr int RING = 4;            // tiles whose steps are kept
 constexpr int BLOCK = 128 * 128;   // bytes of 64 channels of 128 rows
 template <int DH>
 constexpr int QBUF = DH == 64 ? 2 : 1;  // units whose queries are held: what shared memory has room for
+
+// Every row of a unit sees every token of the tile at tok0.
+__device__ __forceinline__ bool all_visible(const AttnKV8Params &p, const KV8Span &span, int tok0)
+{
+    return tok0 + TS - 1 <= span.first && (p.window == 0 || tok0 > span.last - p.window || tok0 + TS - 1 < p.sinks);
+}
+
+// The units of a CTA's part, each warp on its own.  They live in shared memory: few of the fields are
+// needed at a time, and registers are short.
+struct Units {
+    int64_t u0, hi;
+    int b, qt, hk, j0, j1, number;
+    KV8Seq s;
+    KV8Span span;
+    int rows;
+
+    __device__ __forceinline__ void begin(const KV8Start &st)
+    {
+        u0 = st.u0;
+        hi = st.hi;
+        b = st.b;
+        qt = st.qt;
+        hk = st.hk;
+        j0 = st.j0;
+        number = 0;
+    }
+    __device__ __forceinline__ bool open(const AttnKV8Params &p)
+    {
+        if (u0 + EXTRA + j0 >= hi) return false;
+        s = kv8_seq_checked(p.x, b);
+        span = unit_span<TS>(p, s, qt, KV8_TC_ROWS);
+        j1 = static_cast<int>(min(static_cast<int64_t>(span.count), hi - u0 - EXTRA));
+        rows = min(KV8_TC_ROWS, s.n * p.ratio - qt * KV8_TC_ROWS);
+        return true;
+    }
+    __device__ __forceinline__ void close(const AttnKV8Params &p)
+    {
+        ++number;
+        if (j1 < span.count) {
+            u0 = hi;
+            return;
+        }
+        u0 += EXTRA + span.count;
+        j0 = 0;
+        if (u0 + EXTRA < hi) next_unit(p, s, KV8_TC_ROWS, b, qt, hk);
+    }
+    __device__ __forceinline__ int token(int j) const { return TS * (j < span.head ? j : j + span.skip); }
+    __device__ __forceinline__ bool full(const AttnKV8Params &p, int tok0) const { return all_visible(p, span, tok0); }
+};
+
+// The warp's first unit, or (after = true) its next one; false when there is none.
+__device__ __forceinline__ bool take_unit(const AttnKV8Params &p, const KV8Start &st, Units &shared, bool after)
+{
+    Units u;
+    if (after) {
+        u = shared;
+        u.close(p);
+    } else {
+        u.begin(st);
+    }
+    const bool more = u.open(p);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) shared = u;
+    __syncwarp();
+    return more;
+}
 
 template <int DH>
 struct __align__(1024) TcSmem {
     uint8_t k[2][DH / 64][BLOCK];
     uint8_t v[2][DH / 64][BLOCK];
     uint8_t q[QBUF<DH>][2][DH / 64][BLOCK];
-    float4 step[RING][8];                           // per 16 tokens: key step, log2 and inverse of the value step
+    // per 16 tokens: what a product is times to be a base-2 logit (above 0, so that -inf stays -inf), log2 and inverse
+    // of the value step
+    float4 step[RING][8];
     int2 tile[RING];                                // first token; whether every row sees all of the tile
-    float fac[2][256];                              // per unit and row: what a product is times to be a base-2 logit
     int nan_unit[4];                                // number + 1 of the unit whose masked tiles hold NaN values
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t q_full[QBUF<DH>][2], q_empty[QBUF<DH>][2], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[QBUF<DH>][2], q_empty[QBUF<DH>][2], s_full[2], p_half[2], p_full[2], o_done[2], drain;
     uint32_t tmem;
     KV8Start start;
+    Units units[TC_THREADS / 32];
 };
 
 __device__ __forceinline__ constexpr uint32_t idesc_f16(int n)
@@ -110,52 +180,31 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16])
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A bounded wait by whole warps: the lanes go on, or give up, together.
+// A bounded wait by whole warps: the lanes go on, or give up, together.  The warp sleeps in the wait (up to
+// 20 us a try): polling without the hint took a fifth of the kernel's issue slots.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
 {
-    return __any_sync(FULL_MASK, mbar_wait_bounded(bar, parity));
+    unsigned long long t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile("{\n\t.reg .pred p;\n\t"
+                     "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (__any_sync(FULL_MASK, ok)) return true;
+        const unsigned long long t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (__any_sync(FULL_MASK, t - t0 > WAIT_LIMIT_NS)) return false;
+    }
 }
 
-// Registers per thread of the warpgroups, 128 at launch: 2 x 136 + 128 + 112 = 4 x 128.
+// Registers per thread of the warpgroups, 128 at launch: 2 x 136 + 144 + 96 = 4 x 128.
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// Every row of a unit sees every token of the tile at tok0.
-__device__ __forceinline__ bool all_visible(const AttnKV8Params &p, const KV8Span &span, int tok0)
-{
-    return tok0 + TS - 1 <= span.first && (p.window == 0 || tok0 > span.last - p.window || tok0 + TS - 1 < p.sinks);
-}
-
-// The units of a CTA's part, each warp role on its own.
-struct Units {
-    int64_t cur, hi;
-    int b, qt, hk, j0, j1, number;
-    KV8Seq s;
-    KV8Span span;
-    int rows;
-
-    __device__ __forceinline__ Units(const KV8Start &st) : cur(st.lo), hi(st.hi), b(st.b), qt(st.qt), hk(st.hk), j0(st.j0), number(0) {}
-    __device__ __forceinline__ bool open(const AttnKV8Params &p)
-    {
-        if (cur >= hi) return false;
-        s = kv8_seq_checked(p.x, b);
-        span = unit_span<TS>(p, s, qt, KV8_TC_ROWS);
-        j1 = static_cast<int>(min(static_cast<int64_t>(span.count), j0 + (hi - cur)));
-        rows = min(KV8_TC_ROWS, s.n * p.ratio - qt * KV8_TC_ROWS);
-        return true;
-    }
-    __device__ __forceinline__ void close(const AttnKV8Params &p)
-    {
-        cur += j1 - j0;
-        j0 = 0;
-        ++number;
-        if (j1 == span.count && cur < hi) next_unit(p, s, KV8_TC_ROWS, b, qt, hk);
-    }
-    __device__ __forceinline__ int token(int j) const { return TS * (j < span.head ? j : j + span.skip); }
-    __device__ __forceinline__ bool full(const AttnKV8Params &p, int tok0) const { return all_visible(p, span, tok0); }
-};
 
 // Channels 8 c8 .. of a Q, K or V row: 64-channel block and 16-byte place in it.  With 128 channels the block
 // is which half of 16 channels it is, so that the 8 lanes that convert a row's 16-byte loads
@@ -174,79 +223,94 @@ __device__ __forceinline__ int column_channel(int n)
     return DH == 128 ? 16 * ((n >> 3) & 7) + 8 * (n >> 6) : n;
 }
 
+// Each warp converts 32 tokens of a tile, two slices of 16.
 template <int DH>
 __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> &sm, int &flags)
 {
     constexpr int LPR = DH / 16;       // lanes per row
-    constexpr int IT = LPR;            // rows per thread, 128 / LPR apart
-    const int tid = threadIdx.x - CONV0, lane = tid & 31;
-    const int kc = tid % LPR, kr = tid / LPR;
-    const int in_slice = (kr & 15) * DH + 16 * kc;  // the thread's bytes within any 16-token slice
-    const uint32_t dst0 = row_offset<DH>(kr, 2 * kc), dst1 = row_offset<DH>(kr, 2 * kc + 1);
+    constexpr int IT = LPR;            // rows per thread, RPI apart
+    constexpr int RPI = 32 / LPR;
+    const int tid = threadIdx.x - CONV0, lane = tid & 31, warp = tid >> 5;
+    const int kc = lane % LPR, kr = lane / LPR;
+    const uint32_t in_slice = kr * DH + 16 * kc;  // the thread's bytes from a slice's beginning on
+    // where its rows' two pieces go; with 4 rows at a time every other row has another swizzle
+    const uint32_t dst0 = row_offset<DH>(32 * warp + kr, 2 * kc), dst1 = row_offset<DH>(32 * warp + kr, 2 * kc + 1);
+    // keys take the queries' type and the sign of the softmax scale, so that a logit grows with its product
+    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80808080u : 0u;
     int n = 0;  // tiles so far
-    Units u(sm.start);
+    Units u;
     uint4 kw[IT], vw[IT];
-    float ks = 0.0f, vs = 0.0f;
-    int id = -1;            // in lanes 0-7: the page of each slice of the tile being loaded, as the table has it
-    int64_t at = 0;         // in lanes 0-7: where the slice begins in the cache's codes
-    uint32_t none = 0;      // slices without a page (nothing cached there, or a bad page)
+    float ks = 0.0f, vs = 0.0f;     // lanes 0, 1: the steps of the warp's slices
+    int id = -1;                    // in lanes 0, 1: their pages in the tile to be loaded next, as the table has them
+    const uint8_t *k_at[2], *v_at[2];
+    uint32_t none = 0;              // which of them have no page (nothing cached there, or a bad page)
 
     auto page_id = [&](int j) {
-        const int tok = u.token(j) + 16 * (lane & 7);
+        const int tok = u.token(j) + 32 * warp + 16 * (lane & 1);
         return j < u.j1 && tok < u.s.len ? __ldg(p.x.block_table + static_cast<int64_t>(u.b) * p.x.max_pages + (tok >> p.x.page_shift)) : -1;
     };
     // tile j's slices, from the page ids (loaded before)
     auto locate = [&](int j) {
-        const int tok = u.token(j) + 16 * (lane & 7);
+        const int tok = u.token(j) + 32 * warp + 16 * (lane & 1);
         const bool ok = id >= 0 && id < p.x.num_pages;
         if (!ok && tok < u.s.len) flags |= ST_CACHE_INDEX;
-        none = __ballot_sync(FULL_MASK, !ok) & 0xffu;
+        none = __ballot_sync(FULL_MASK, !ok) & 3u;
         const int64_t ph = static_cast<int64_t>(ok ? id : 0) * p.Hkv + u.hk;
-        at = ((ph << p.x.page_shift) + (tok & ((1 << p.x.page_shift) - 1))) * DH;
-        if (tid < 8) {
+        const int64_t at = ((ph << p.x.page_shift) + (tok & ((1 << p.x.page_shift) - 1))) * DH;
+        if (lane < 2) {
             ks = __ldg(p.k_steps + ph);
             vs = __ldg(p.v_steps + ph);
         }
-    };
-    auto load = [&](uint4 (&w)[IT], const uint8_t *codes) {
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int64_t slice = __shfl_sync(FULL_MASK, at, (kr >> 4) + i * (8 / IT));
-            w[i] = __ldg(reinterpret_cast<const uint4 *>(codes + slice + in_slice));
+        for (int i = 0; i < 2; ++i) {
+            const int64_t slice = __shfl_sync(FULL_MASK, at, i) + in_slice;
+            k_at[i] = p.k_codes + slice;
+            v_at[i] = p.v_codes + slice;
         }
+    };
+    auto load = [&](uint4 (&w)[IT], const uint8_t *const (&at)[2]) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(at[i / (IT / 2)] + (i % (IT / 2)) * RPI * DH));
     };
     // rows of slices that `gone` names, and rows from `end` on, become zero
     auto clear = [&](uint4 (&w)[IT], uint32_t gone, int end) {
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int r = kr + i * (128 / LPR);
-            if (((gone >> (r >> 4)) & 1) || r >= end) w[i] = make_uint4(0, 0, 0, 0);
-        }
+        for (int i = 0; i < IT; ++i)
+            if (((gone >> (i / (IT / 2))) & 1) || 32 * warp + kr + i * RPI >= end) w[i] = make_uint4(0, 0, 0, 0);
     };
-    auto store = [&](uint8_t *dst, const uint4 (&w)[IT]) {
+    auto store = [&](uint8_t *dst, const uint4 (&w)[IT], uint32_t signs, bool bf16) {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            const uint32_t x[4] = {w[i].x ^ signs, w[i].y ^ signs, w[i].z ^ signs, w[i].w ^ signs};
             uint32_t h[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 h[2 * k] = e4m3x2_to_half2(x[k] & 0xffffu);
                 h[2 * k + 1] = e4m3x2_to_half2(x[k] >> 16);
             }
-            *reinterpret_cast<uint4 *>(dst + dst0 + i * (128 / LPR) * 128) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(dst + dst1 + i * (128 / LPR) * 128) = make_uint4(h[4], h[5], h[6], h[7]);
+            if (bf16) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                    h[k] = pack_bf16x2(v.x, v.y);
+                }
+            }
+            const uint32_t turn = (i * RPI & 7) << 4;
+            *reinterpret_cast<uint4 *>(dst + (dst0 ^ turn) + i * RPI * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(dst + (dst1 ^ turn) + i * RPI * 128) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         fence_proxy_async_smem();
         __syncwarp();
     };
 
+    u.begin(sm.start);
     bool more = u.open(p);
     int j = u.j0;
     if (more) {
         id = page_id(j);
         locate(j);
-        load(kw, p.k_codes);
-        load(vw, p.v_codes);
+        load(kw, k_at);
+        load(vw, v_at);
         id = page_id(j + 1);
     }
     while (more) {
@@ -256,14 +320,17 @@ __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> 
         const bool full = u.full(p, tok0);
         const uint32_t gone = none;
         if (!warp_wait(smem_addr(&sm.k_empty[st]), par)) return false;
-        if (tid < 8) {
-            const bool here = !((none >> tid) & 1);
+        if (lane < 2) {
+            const bool here = !((gone >> lane) & 1);
             const float k1 = fminf(fmaxf(ks, KV8_STEP_MIN), KV8_STEP_MAX), v1 = fminf(fmaxf(vs, KV8_STEP_MIN), KV8_STEP_MAX);
-            sm.step[n % RING][tid] = make_float4(here ? k1 : 0.0f, here ? lg2(v1) : -INFINITY, here ? 1.0f / v1 : 0.0f, 0.0f);
+            sm.step[n % RING][2 * warp + lane] = make_float4(fmaxf(here ? k1 * fabsf(p.scale_log2) : 0.0f, 1.17549435e-38f), here ? lg2(v1) : -INFINITY, here ? 1.0f / v1 : 0.0f, 0.0f);
             if (tid == 0) sm.tile[n % RING] = make_int2(tok0, full);
         }
         if (gone) clear(kw, gone, 128);
-        store(&sm.k[st][0][0], kw);
+        if (p.half)
+            store(&sm.k[st][0][0], kw, flip, false);
+        else
+            store(&sm.k[st][0][0], kw, flip, true);
         if (lane == 0) mbar_arrive(smem_addr(&sm.k_full[st]));
         // on to the next tile, of this unit or the next one
         if (++j == u.j1) {
@@ -274,7 +341,7 @@ __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> 
         }
         if (more) {
             locate(j);
-            load(kw, p.k_codes);
+            load(kw, k_at);
             id = page_id(j + 1);
         }
         if (!full) {
@@ -298,156 +365,127 @@ __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> 
             clear(vw, gone, 128);
         }
         if (!warp_wait(smem_addr(&sm.v_empty[st]), par)) return false;
-        store(&sm.v[st][0][0], vw);
+        store(&sm.v[st][0][0], vw, 0u, false);
         if (lane == 0) mbar_arrive(smem_addr(&sm.v_full[st]));
-        if (more) load(vw, p.v_codes);
+        if (more) load(vw, v_at);
         ++n;
     }
     return true;
 }
 
-__device__ __forceinline__ uint32_t bf16_pair_to_half(uint32_t w, float f)
-{
-    return pack16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f, true);
-}
-
-// Queries of the units, a row on DH / 8 lanes: fp16 as they are, bf16 scaled by a power of two per row
-// into fp16's range; with the sign of the softmax scale, so that a row's factor is not negative.
+// Query tile t of each unit, as it is, into the swizzled rows; rows that the unit has not become zero.
 template <int DH>
-__device__ __forceinline__ bool query_role(const AttnKV8Params &p, TcSmem<DH> &sm)
+__device__ __forceinline__ bool query_role(const AttnKV8Params &p, TcSmem<DH> &sm, int t)
 {
-    constexpr int LPR = DH / 8, RPW = 32 / LPR, STRIDE = QLOAD_WARPS * RPW, BATCH = 6;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x - QLOAD0) >> 5;
-    const int c8 = lane % LPR, first = warp * RPW + lane / LPR;
-    const uint32_t flip = p.scale_log2 < 0.0f ? 0x80008000u : 0u;
-    const float scale = fabsf(p.scale_log2);
-    int un[QBUF<DH>][2] = {};
-    Units u(sm.start);
-    for (; u.open(p); u.close(p)) {
-        const int buf = u.number % QBUF<DH>;
+    constexpr int LPR = DH / 8, RPI = 32 / LPR;
+    const int lane = threadIdx.x & 31, c8 = lane % LPR, rl = lane / LPR;
+    uint32_t phase = 0;  // bit buf: parity of that place's turn
+    Units &u = sm.units[threadIdx.x >> 5];
+    for (bool more = take_unit(p, sm.start, u, false); more; more = take_unit(p, sm.start, u, true)) {
+        const int buf = u.number % QBUF<DH>, rows = min(128, u.rows - t * 128);
+        if (rows <= 0) continue;
+        const int rr0 = u.qt * KV8_TC_ROWS + t * 128, token0 = p.div_ratio(rr0);
+        const uint16_t *src = p.q + (static_cast<int64_t>(u.s.q0 + token0) * p.Hq + u.hk * p.ratio + rr0 - token0 * p.ratio) * DH + 8 * c8;
+        const uint32_t dst = smem_addr(&sm.q[buf][t][0][0]);
+        if (!warp_wait(smem_addr(&sm.q_empty[buf][t]), ((phase >> buf) & 1) ^ 1)) return false;
+        phase ^= 1u << buf;
+#pragma unroll 2
+        for (int r8 = 0; r8 < 128; r8 += 8) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            if (t * 128 >= u.rows) break;
-            const int rows = min(128, u.rows - t * 128);
-            int &turn = un[QBUF<DH> == 1 ? 0 : buf][t];
-            const int rr0 = u.qt * KV8_TC_ROWS + t * 128, token0 = p.div_ratio(rr0);
-            const uint16_t *src = p.q + (static_cast<int64_t>(u.s.q0 + token0) * p.Hq + u.hk * p.ratio + rr0 - token0 * p.ratio) * DH + 8 * c8;
-            uint8_t *dst = &sm.q[buf][t][0][0];
-            bool waited = turn == 0;
-#pragma unroll 1
-            for (int r0 = first; r0 < 128; r0 += STRIDE * BATCH) {
-                uint4 w[BATCH];
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int r = r0 + i * STRIDE;
-                    // at most 128 tokens of 2^16 heads on: 32 bits
-                    const uint32_t off = static_cast<uint32_t>(r + (p.div_ratio(rr0 + r) - token0) * (p.Hq - p.ratio)) * DH;
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (r < rows) w[i] = __ldg(reinterpret_cast<const uint4 *>(src + off));
-                }
-                if (!waited && !warp_wait(smem_addr(&sm.q_empty[buf][t]), (turn - 1) & 1)) return false;
-                waited = true;
-                float up[BATCH];
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) up[i] = scale;
-                if (!p.half) {
-                    uint32_t top[BATCH];
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        // non-negative bf16 pairs compare as they are in the upper half, the lower one shifted there
-                        const uint32_t a = w[i].x & 0x7fff7fffu, b = w[i].y & 0x7fff7fffu, c = w[i].z & 0x7fff7fffu, d = w[i].w & 0x7fff7fffu;
-                        top[i] = max(max(max(a, b), max(c, d)), max(max(a << 16, b << 16), max(c << 16, d << 16)));
-                    }
-#pragma unroll
-                    for (int o = 1; o < LPR; o <<= 1)
-#pragma unroll
-                        for (int i = 0; i < BATCH; ++i) top[i] = max(top[i], __shfl_xor_sync(FULL_MASK, top[i], o));
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        // a row that is not finite stays so under any factor
-                        const int e = row_exponent(__uint_as_float(min(top[i] & 0xffff0000u, 0x7f7f0000u)));
-                        const float f = exp2i(-e);
-                        up[i] = scale * exp2i(e);
-                        w[i].x = bf16_pair_to_half(w[i].x, f);
-                        w[i].y = bf16_pair_to_half(w[i].y, f);
-                        w[i].z = bf16_pair_to_half(w[i].z, f);
-                        w[i].w = bf16_pair_to_half(w[i].w, f);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int r = r0 + i * STRIDE;
-                    if (r < 128) {
-                        *reinterpret_cast<uint4 *>(dst + row_offset<DH>(r, c8)) =
-                            make_uint4(w[i].x ^ flip, w[i].y ^ flip, w[i].z ^ flip, w[i].w ^ flip);
-                        if (c8 == 0) sm.fac[u.number & 1][t * 128 + r] = up[i];
-                    }
-                }
+            for (int i = 0; i < 8; i += RPI) {
+                const int r = r8 + i + rl;
+                // at most 128 tokens of 2^16 heads on: 32 bits
+                const bool in = r < rows;
+                const uint32_t off = in ? static_cast<uint32_t>(r + (p.div_ratio(rr0 + r) - token0) * (p.Hq - p.ratio)) * DH : 0u;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r8 * 128 + row_offset<DH>(i + rl, c8)), "l"(src + off), "r"(in ? 16 : 0)
+                             : "memory");
             }
-            ++turn;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[buf][t]));
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sm.q_full[buf][t]));
     }
     return true;
 }
 
+// The MMAs of query tile t, tile by tile: the tile before's values, then the tile's scores (which take the
+// columns that P leaves).
 template <int DH>
-__device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm, uint32_t tmem)
+__device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm, uint32_t tmem, int t)
 {
-    const uint32_t id_s = idesc_f16(TS), id_o = idesc_f16(DH) | (1u << 16);  // V: channels-major
+    const uint32_t id_s = p.half ? idesc_f16(TS) : idesc_bf16(TS), id_o = idesc_f16(DH) | (1u << 16);  // V: channels-major
     // K, Q: rows of 64 channels, 8-row groups 1024 bytes apart; V: 64 channels of a token a row, 8-token
     // groups 1024 bytes, 64-channel blocks BLOCK bytes apart
-    const uint64_t q0 = sw128_desc(smem_addr(&sm.q[0][0][0][0])), k0 = sw128_desc(smem_addr(&sm.k[0][0][0]));
-    const uint64_t v0 = (sw128_desc(smem_addr(&sm.v[0][0][0])) & ~(0x3fffull << 16)) | (static_cast<uint64_t>(BLOCK >> 4) << 16);
     constexpr uint64_t STAGE = (DH / 64) * (BLOCK >> 4);
-    int n = 0, cnt[2] = {0, 0}, un[QBUF<DH>][2] = {};  // tiles; tiles and units of each query tile
-    Units u(sm.start);
-    while (u.open(p)) {
-        const int last_t = u.rows > 128 ? 1 : 0, buf = u.number % QBUF<DH>;
+    const uint64_t k0 = sw128_desc(smem_addr(&sm.k[0][0][0]));
+    const uint64_t v0 = (sw128_desc(smem_addr(&sm.v[0][0][0])) & ~(0x3fffull << 16)) | (static_cast<uint64_t>(BLOCK >> 4) << 16);
+    const uint32_t s_cols = tmem + t * TS, o_cols = tmem + 2 * TS + t * DH;
+    int n = 0;
+    uint32_t q_phase = 0, p_phase = 0;  // parities: bit buf; bit 0
+    Units &u = sm.units[threadIdx.x >> 5];
+    for (bool more = take_unit(p, sm.start, u, false); more; more = take_unit(p, sm.start, u, true)) {
+        const int tiles = u.j1 - u.j0, buf = u.number % QBUF<DH>;
+        if (t * 128 >= u.rows) {
+            // nothing to do but to let the tiles go
 #pragma unroll 1
-        for (int j = u.j0; j <= u.j1; ++j, ++n) {
-            // tile j - 1's values, then tile j's scores (which take the columns that P leaves)
+            for (int j = 0; j < tiles; ++j, ++n) {
+                if (!warp_wait(smem_addr(&sm.k_full[n & 1]), (n >> 1) & 1)) return false;
+                if (elect_one()) mbar_arrive(smem_addr(&sm.k_empty[n & 1]));
+                if (!warp_wait(smem_addr(&sm.v_full[n & 1]), (n >> 1) & 1)) return false;
+                if (elect_one()) mbar_arrive(smem_addr(&sm.v_empty[n & 1]));
+                __syncwarp();
+            }
+            continue;
+        }
+        const uint64_t q = sw128_desc(smem_addr(&sm.q[buf][t][0][0]));
+        if (!warp_wait(smem_addr(&sm.q_full[buf][t]), (q_phase >> buf) & 1)) return false;
+        q_phase ^= 1u << buf;
+#pragma unroll 1
+        for (int j = 0; j <= tiles; ++j, ++n) {
             const int st = n & 1;
+            if (j > 0) {
+                const uint64_t v = v0 + (st ^ 1) * STAGE;
+                const uint32_t add = j > 1 ? 1u : 0u;
+                if (!warp_wait(smem_addr(&sm.v_full[st ^ 1]), ((n - 1) >> 1) & 1)) return false;
+                if (!warp_wait(smem_addr(&sm.p_half[t]), p_phase)) return false;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (t > last_t) break;
-                if (j > u.j0) {
-                    if (t == 0 && !mbar_wait_bounded(smem_addr(&sm.v_full[st ^ 1]), ((n - 1) >> 1) & 1)) return false;
-                    if (!mbar_wait_bounded(smem_addr(&sm.p_full[t]), cnt[t] & 1)) return false;
-                    ++cnt[t];
-                    tc_fence_after();
-                    const uint64_t v = v0 + (st ^ 1) * STAGE;
-#pragma unroll
-                    for (int s = 0; s < TS / 16; ++s)
-                        mma_f16_ts(tmem + 2 * TS + t * DH, tmem + t * TS + TS / 2 + 8 * s, v + s * (16 * 128 >> 4), id_o,
-                                   s || j - 1 > u.j0 ? 1u : 0u);
-                    if (t == last_t) mma_commit(smem_addr(&sm.v_empty[st ^ 1]));
-                    if (j == u.j1) mma_commit(smem_addr(&sm.o_done[t]));
-                } else {
-                    int &turn = un[QBUF<DH> == 1 ? 0 : buf][t];
-                    if (!mbar_wait_bounded(smem_addr(&sm.q_full[buf][t]), turn & 1)) return false;
-                    ++turn;
+                    for (int s = TS / 32; s < TS / 16; ++s)
+                        mma_f16_ts(o_cols, s_cols + TS / 2 + 8 * s, v + s * (16 * 128 >> 4), id_o, s > TS / 32 ? 1u : add);
                 }
-                if (j < u.j1) {
-                    if (t == 0 && !mbar_wait_bounded(smem_addr(&sm.k_full[st]), (n >> 1) & 1)) return false;
-                    tc_fence_after();
-                    const uint64_t q = q0 + (2 * buf + t) * STAGE, k = k0 + st * STAGE;
+                __syncwarp();
+                if (!warp_wait(smem_addr(&sm.p_full[t]), p_phase)) return false;
+                p_phase ^= 1u;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < TS / 32; ++s) mma_f16_ts(o_cols, s_cols + TS / 2 + 8 * s, v + s * (16 * 128 >> 4), id_o, 1u);
+                    mma_commit(smem_addr(&sm.v_empty[st ^ 1]));
+                    if (j == tiles) mma_commit(smem_addr(&sm.o_done[t]));
+                }
+                __syncwarp();
+            }
+            if (j < tiles) {
+                const uint64_t k = k0 + st * STAGE;
+                if (!warp_wait(smem_addr(&sm.k_full[st]), (n >> 1) & 1)) return false;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < DH / 16; ++s) {
                         const uint32_t off = ((s >> 2) * BLOCK + (s & 3) * 32) >> 4;
-                        mma_bf16(tmem + t * TS, q + off, k + off, id_s, s ? 1u : 0u);
+                        mma_bf16(s_cols, q + off, k + off, id_s, s ? 1u : 0u);
                     }
                     // done when all before it is, the last tile's values among that
                     mma_commit(smem_addr(&sm.s_full[t]));
-                    if (t == last_t) mma_commit(smem_addr(&sm.k_empty[st]));
-                    if (j + 1 == u.j1) mma_commit(smem_addr(&sm.q_empty[buf][t]));
+                    mma_commit(smem_addr(&sm.k_empty[st]));
+                    if (j + 1 == tiles) mma_commit(smem_addr(&sm.q_empty[buf][t]));
                 }
+                __syncwarp();
             }
         }
         --n;
-        u.close(p);
     }
     return true;
 }
@@ -483,35 +521,46 @@ struct RowMask {
     __device__ __forceinline__ uint32_t bits(int c0) const { return below(hi - c0) & (~below(lo - c0) | below(sk - c0)); }
 };
 
+// Columns that the row does not see become -inf.
+__device__ __forceinline__ void hide(uint32_t (&raw)[32], uint32_t bits)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i) raw[i] = (bits >> i) & 1 ? raw[i] : 0xff800000u;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The largest base-2 logit (without the maximum's offset) of 32 columns.
-template <bool MASKED>
-__device__ __forceinline__ float chunk_top(const uint32_t (&raw)[32], const float4 *step, float fac, uint32_t bits)
+__device__ __forceinline__ float chunk_top(const uint32_t (&raw)[32], const float4 *step)
 {
     float top = -INFINITY;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        float x[16];
+        float x[2] = {__uint_as_float(raw[16 * g]), __uint_as_float(raw[16 * g + 1])};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            x[i] = __uint_as_float(raw[16 * g + i]);
-            if (MASKED && !((bits >> (16 * g + i)) & 1)) x[i] = -INFINITY;
+        for (int i = 2; i < 16; i += 4) {
+            x[0] = max3(x[0], __uint_as_float(raw[16 * g + i]), __uint_as_float(raw[16 * g + i + 1]));
+            if (i + 2 < 16) x[1] = max3(x[1], __uint_as_float(raw[16 * g + i + 2]), __uint_as_float(raw[16 * g + i + 3]));
         }
-#pragma unroll
-        for (int i = 1; i < 16; ++i) x[0] = fmaxf(x[0], x[i]);
-        // the factor is not negative and rounding keeps order: the logit of the maximum
-        top = fmaxf(top, __fmaf_rn(x[0], fac * step[g].x, step[g].y));
+        // the factor is positive and rounding keeps order: the logit of the maximum
+        top = fmaxf(top, __fmaf_rn(fmaxf(x[0], x[1]), step[g].x, step[g].y));
     }
     return top;
 }
 
 // P of 32 columns as fp16 pairs, and their part of the row's sum.
-template <bool MASKED>
-__device__ __forceinline__ void chunk_p(const uint32_t (&raw)[32], const float4 *step, float fac, float m, uint32_t bits,
+__device__ __forceinline__ void chunk_p(const uint32_t (&raw)[32], const float4 &step0, const float4 &step1, float m,
                                         uint32_t (&pw)[16], float &l)
 {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-        const float f = fac * step[g].x, a = step[g].y - m;
+        const float4 &step = g ? step1 : step0;
+        const float f = step.x, a = step.y - m;
         const uint64_t f2 = pair(f, f), a2 = pair(a, a);
         uint64_t sum = 0;
 #pragma unroll
@@ -521,16 +570,12 @@ __device__ __forceinline__ void chunk_p(const uint32_t (&raw)[32], const float4 
             unpair(fma_pair(pair(__uint_as_float(raw[k]), __uint_as_float(raw[k + 1])), f2, a2), x, y);
             x = ex2(x);
             y = ex2(y);
-            if (MASKED) {
-                x = (bits >> k) & 1 ? x : 0.0f;
-                y = (bits >> (k + 1)) & 1 ? y : 0.0f;
-            }
             sum = add_pair(sum, pair(x, y));
             pw[8 * g + i] = pack16(x, y, true);
         }
         float x, y;
         unpair(sum, x, y);
-        l = __fmaf_rn(x + y, step[g].z, l);
+        l = __fmaf_rn(x + y, step.z, l);
     }
 }
 
@@ -540,10 +585,11 @@ struct RowState {
     float m, l, pass;
 };
 
-// S of one tile to P, the row's thread.
+// S of one tile to P, the row's thread.  (Tiles that every row sees whole have code of their own: with the
+// masking in it, skipped as it was, the same loop took a fifth longer.)
 template <int DH, bool MASKED>
-__device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_full, bool first, uint32_t s_cols, uint32_t o_cols,
-                                             float fac, const RowMask &mask, RowState &r)
+__device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_half, uint32_t p_full, bool first, uint32_t s_cols,
+                                             uint32_t o_cols, const RowMask &mask, RowState &r)
 {
     uint32_t a[32], b[32], pw[16];
     tmem_ld32_async(s_cols, a);
@@ -553,9 +599,13 @@ __device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_full
     for (int h = 0; h < 2; ++h) {
         tmem_ld_wait(a);
         tmem_ld_wait(b);
-        top = fmaxf(top, chunk_top<MASKED>(a, step + 4 * h, fac, MASKED ? mask.bits(64 * h) : 0u));
+        if (MASKED) {
+            hide(a, mask.bits(64 * h));
+            hide(b, mask.bits(64 * h + 32));
+        }
+        top = fmaxf(top, chunk_top(a, step + 4 * h));
         if (h == 0) tmem_ld32_async(s_cols + 64, a);
-        top = fmaxf(top, chunk_top<MASKED>(b, step + 4 * h + 2, fac, MASKED ? mask.bits(64 * h + 32) : 0u));
+        top = fmaxf(top, chunk_top(b, step + 4 * h + 2));
         if (h == 0) tmem_ld32_async(s_cols + 96, b);
     }
     const bool moves = top > r.pass;
@@ -563,7 +613,7 @@ __device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_full
         // the maximum moves: a whole number, so that every factor is a power of two (before a row's
         // first logit there is nothing to rescale)
         const float to = moves ? ceilf(top) : r.m;
-        const float alpha = moves && r.pass > -INFINITY ? ex2(r.m - to) : 1.0f;
+        const float alpha = !moves ? 1.0f : r.pass > -INFINITY ? ex2(r.m - to) : 0.0f;
         if (moves) {
             r.m = to;
             r.pass = to + 8.0f;
@@ -584,21 +634,26 @@ __device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_full
     // backwards: the last two chunks are at hand, and P takes the upper columns once they are read
 #pragma unroll 1
     for (int h = 1; h >= 0; --h) {
+        const float4 c0 = step[4 * h], c1 = step[4 * h + 1], c2 = step[4 * h + 2], c3 = step[4 * h + 3];
         if (h == 0) {
             tmem_ld_wait(a);
             tmem_ld_wait(b);
+            if (MASKED) {
+                hide(a, mask.bits(0));
+                hide(b, mask.bits(32));
+            }
         }
-        chunk_p<MASKED>(b, step + 4 * h + 2, fac, r.m, MASKED ? mask.bits(64 * h + 32) : 0u, pw, r.l);
+        chunk_p(b, c2, c3, r.m, pw, r.l);
         if (h == 1) tmem_ld32_async(s_cols + 32, b);
         tmem_st16(s_cols + TS / 2 + 32 * h + 16, pw);
-        chunk_p<MASKED>(a, step + 4 * h, fac, r.m, MASKED ? mask.bits(64 * h) : 0u, pw, r.l);
+        chunk_p(a, c0, c1, r.m, pw, r.l);
         if (h == 1) tmem_ld32_async(s_cols, a);
         tmem_st16(s_cols + TS / 2 + 32 * h, pw);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(h ? p_half : p_full);
     }
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(p_full);
 }
 
 // Which of the 8 channels from ch on have a NaN value code that a row at index `at` sees in tiles
@@ -633,32 +688,30 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
     const uint32_t lanes = tmem + (static_cast<uint32_t>(r & 96) << 16);
     const uint32_t s_cols = lanes + t * TS, o_cols = lanes + 2 * TS + t * DH;
     int n = 0, cnt = 0, unit = 0;  // tiles of the part; tiles and units of this query tile
-    Units u(sm.start);
-    for (; u.open(p); u.close(p)) {
+    Units &u = sm.units[threadIdx.x >> 5];
+    for (bool more = take_unit(p, sm.start, u, false); more; more = take_unit(p, sm.start, u, true)) {
+        const int tiles = u.j1 - u.j0;
         if (t * 128 >= u.rows) {
-            n += u.j1 - u.j0;
+            n += tiles;
             continue;
         }
         const int row = t * 128 + r;
         const bool live = row < u.rows;
-        const int rr = u.qt * KV8_TC_ROWS + row;
-        const int token = p.div_ratio(rr), at = live ? u.s.len - u.s.n + token : -1;
+        const int at = live ? u.s.len - u.s.n + p.div_ratio(u.qt * KV8_TC_ROWS + row) : -1;
         RowState st{0.0f, 0.0f, -INFINITY};
-        float fac = 0.0f;
 #pragma unroll 1
-        for (int j = u.j0; j < u.j1; ++j, ++n, ++cnt) {
+        for (int j = 0; j < tiles; ++j, ++n, ++cnt) {
             if (!warp_wait(smem_addr(&sm.s_full[t]), cnt & 1)) return false;
             tc_fence_after();
-            const bool first = j == u.j0;
-            if (first) fac = sm.fac[u.number & 1][row];
+            const bool first = j == 0;
             const int2 tile = sm.tile[n % RING];
             const int hi = at - tile.x + 1;
             const RowMask mask{hi, p.window ? hi - p.window : 0, p.window ? p.sinks - tile.x : 0};
-            const uint32_t p_full = smem_addr(&sm.p_full[t]);
+            const uint32_t p_half = smem_addr(&sm.p_half[t]), p_full = smem_addr(&sm.p_full[t]);
             if (tile.y)
-                softmax_tile<DH, false>(sm.step[n % RING], p_full, first, s_cols, o_cols, fac, mask, st);
+                softmax_tile<DH, false>(sm.step[n % RING], p_half, p_full, first, s_cols, o_cols, mask, st);
             else
-                softmax_tile<DH, true>(sm.step[n % RING], p_full, first, s_cols, o_cols, fac, mask, st);
+                softmax_tile<DH, true>(sm.step[n % RING], p_half, p_full, first, s_cols, o_cols, mask, st);
         }
 
         // ---- the unit's end ------------------------------------------------------------------------
@@ -669,17 +722,17 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
         const bool nan = *reinterpret_cast<volatile int *>(&sm.nan_unit[u.number & 3]) == u.number + 1;
         const bool empty = st.pass == -INFINITY && st.l == 0.0f;
         const float top = st.pass == -INFINITY ? -INFINITY : st.m;
+        const int rr = u.qt * KV8_TC_ROWS + row, token = p.div_ratio(rr);
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u.number == 0 ? 0 : 1);
         const int64_t q_row = static_cast<int64_t>(u.s.q0) * p.Hq + u.hk * p.ratio + rr + static_cast<int64_t>(token) * (p.Hq - p.ratio);
         const float inv = empty ? 0.0f : 1.0f / st.l;
 #pragma unroll 1
-        for (int c = 0; c < DH; c += 32) {
-            uint32_t raw[32];
-            tmem_ld32_async(o_cols + c, raw);
-            tmem_ld_wait(raw);
+        for (int c = 0; c < DH; c += 16) {
+            uint32_t raw[16];
+            tmem_ld16(o_cols + c, raw);
             if (!live) continue;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < 2; ++g) {
                 const int ch = column_channel<DH>(c + 8 * g);
                 float o[8];
 #pragma unroll
@@ -701,8 +754,12 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
                 }
             }
         }
-        if (live && whole && p.lse) p.lse[q_row] = empty ? -INFINITY : (lg2(st.l) + top) * 0.6931471805599453f;
-        if (live && !whole) *reinterpret_cast<float2 *>(part.ml + (slot * KV8_TC_ROWS + row) * 2) = make_float2(top, st.l);
+        if (live) {
+            if (!whole)
+                *reinterpret_cast<float2 *>(part.ml + (slot * KV8_TC_ROWS + row) * 2) = make_float2(top, st.l);
+            else if (p.lse)
+                p.lse[q_row] = empty ? -INFINITY : (lg2(st.l) + top) * 0.6931471805599453f;
+        }
         tc_fence_before();
     }
     return true;
@@ -713,34 +770,35 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid
 {
     extern __shared__ uint8_t smem_raw[];
     TcSmem<DH> &sm = *reinterpret_cast<TcSmem<DH> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
     wait_prior_grid();
     if (threadIdx.x == 0) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sm.k_full[i]), 4);
             mbar_init(smem_addr(&sm.v_full[i]), 4);
-            mbar_init(smem_addr(&sm.k_empty[i]), 1);
-            mbar_init(smem_addr(&sm.v_empty[i]), 1);
+            mbar_init(smem_addr(&sm.k_empty[i]), 2);
+            mbar_init(smem_addr(&sm.v_empty[i]), 2);
 #pragma unroll
             for (int b = 0; b < QBUF<DH>; ++b) {
-                mbar_init(smem_addr(&sm.q_full[b][i]), QLOAD_WARPS);
+                mbar_init(smem_addr(&sm.q_full[b][i]), 1);
                 mbar_init(smem_addr(&sm.q_empty[b][i]), 1);
             }
             mbar_init(smem_addr(&sm.s_full[i]), 1);
+            mbar_init(smem_addr(&sm.p_half[i]), 4);
             mbar_init(smem_addr(&sm.p_full[i]), 4);
             mbar_init(smem_addr(&sm.o_done[i]), 1);
         }
-        mbar_init(smem_addr(&sm.drain), 1);
+        mbar_init(smem_addr(&sm.drain), 2);
         fence_mbar_init();
 #pragma unroll
         for (int i = 0; i < 4; ++i) sm.nan_unit[i] = 0;
     }
-    if (warp == 12) {
+    if (warp == MMA_WARP) {
         tmem_alloc(smem_addr(&sm.tmem), 512);
         tmem_relinquish();
     }
-    find_start<TS, KV8_TC_ROWS, TC_THREADS>(p, sm.start, 1);
+    find_start<TS, KV8_TC_ROWS, TC_THREADS>(p, sm.start, EXTRA, 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -748,25 +806,26 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid
     const uint32_t tmem = sm.tmem;
     const KV8Partials part(p.workspace, gridDim.x, KV8_TC_ROWS, DH);
     if (threadIdx.x == 0)
-        part.meta[blockIdx.x] = KV8Meta{sm.start.lo, sm.start.hi > sm.start.lo ? sm.start.j0 : 0, sm.start.b, sm.start.qt, sm.start.hk};
+        part.meta[blockIdx.x] = KV8Meta{sm.start.u0, sm.start.j0, sm.start.b, sm.start.qt, sm.start.hk};
 
     int flags = threadIdx.x == 0 ? sm.start.flags : 0;
     bool ok = true;
     if (warp < 8) {
         more_registers<136>();
         ok = softmax_role<DH>(p, sm, tmem, part);
-    } else if (warp < 12) {
-        fewer_registers<128>();
+    } else if (warp < MMA_WARP) {
+        more_registers<144>();
         ok = convert_role<DH>(p, sm, flags);
     } else {
-        fewer_registers<112>();
-        if (warp > 12) {
-            ok = query_role<DH>(p, sm);
-        } else if (lane == 0) {
-            ok = mma_role<DH>(p, sm, tmem);
+        fewer_registers<96>();
+        if (warp >= QUERY_WARP) {
+            ok = query_role<DH>(p, sm, warp - QUERY_WARP);
+        } else {
+            ok = mma_role<DH>(p, sm, tmem, warp - MMA_WARP);
             // nothing of this CTA runs on when its tensor memory goes
-            mma_commit(smem_addr(&sm.drain));
-            ok &= mbar_wait_bounded(smem_addr(&sm.drain), 0);
+            if (elect_one()) mma_commit(smem_addr(&sm.drain));
+            __syncwarp();
+            ok &= warp_wait(smem_addr(&sm.drain), 0);
         }
         __syncwarp();
     }
@@ -775,7 +834,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

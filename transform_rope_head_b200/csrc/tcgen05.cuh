@@ -43,6 +43,15 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
         : "memory");
 }
 
+// One lane of the (converged) warp, the same each time: what it alone issues needs no loop over lanes
+// to bring its operands into uniform registers.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r)::"memory");
+    return r != 0;
+}
+
 // Arrive on the mbarrier once every MMA this thread issued before has completed.
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
