@@ -369,7 +369,8 @@ __global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p
                 acc.w = __fmaf_rn(v.w, f, acc.w);
             }
             if (whole) {
-                store_row(p, s, qt * R + row, hk, c, DH, acc, top, sum);
+                const float o4[4] = {acc.x, acc.y, acc.z, acc.w};
+                store_row<4>(p, s, qt * R + row, hk, c, DH, o4, top, sum);
             } else {
                 *reinterpret_cast<float4 *>(part.o + (slot * R + row) * DH + c) = acc;
                 if (c == 0) *reinterpret_cast<float2 *>(part.ml + (slot * R + row) * 2) = make_float2(top, sum);
@@ -387,113 +388,76 @@ __global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p
     }
 }
 
-// Joins the partial rows of the units that a boundary between two CTAs cuts.  CTA (i, row):
-// boundary i opens the unit's second part, or does nothing.
-template <int DH>
+// Joins the partial rows of the units that a boundary between two CTAs cuts: boundary i does it for the unit
+// whose second part it opens.  G warps take a row (their lanes DH / 32 channels each, a warp every G-th part):
+// 8 where a unit of few rows may have a part on every SM, whose loads are then in flight together, 1 for
+// the many rows and few parts of the tensor-memory kernel.
+template <int DH, int G>
 __global__ void __launch_bounds__(256) k_attention_kv8_join(const AttnKV8Params p, int ctas, int R)
 {
-    constexpr int G = 256 / (DH / 4);  // partials taken side by side
-    __shared__ float s_m[256], s_l[G];
-    __shared__ __align__(16) float s_o[G][DH];
+    constexpr int CPL = DH / 32;
+    __shared__ float s_sum[8], s_acc[8][DH];
     wait_prior_grid();
+    allow_next_grid();
     const KV8Partials part(p.workspace, ctas, R, DH);
-    const int i = blockIdx.x + 1;
-    const KV8Meta me = part.meta[i];
-    if (me.j0 == 0) return;
-    const KV8Meta prev = part.meta[i - 1];
-    if (prev.j0 > 0 && prev.u0 == me.u0) return;
-    const KV8Seq s = kv8_seq_checked(p.x, me.b);
-    const int row = blockIdx.y;
-    if (me.qt * R + row >= s.n * p.ratio) return;
+    const int i = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const KV8Meta me = part.meta[i], prev = part.meta[i - 1];
+    if (me.j0 == 0 || (prev.j0 > 0 && prev.u0 == me.u0)) return;
     int count = 2;  // CTA i - 1, i, and those that go on with the unit
-    while (i - 1 + count < ctas) {
-        const KV8Meta c = part.meta[i - 1 + count];
-        if (c.j0 == 0 || c.u0 != me.u0) break;
-        ++count;
+    for (bool on = true; on; ) {
+        const int k = i - 1 + count + lane;
+        const bool goes = k < ctas && part.meta[k].j0 != 0 && part.meta[k].u0 == me.u0;
+        const int n = __ffs(~__ballot_sync(FULL_MASK, goes)) - 1;  // -1: all 32
+        count += n < 0 ? 32 : n;
+        on = n < 0;
     }
-    auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(i - 1) + (prev.u0 == me.u0 ? 0 : 1) : 2 * static_cast<int64_t>(i - 1 + k); };
-    float top = -INFINITY;
-    for (int k = threadIdx.x; k < count; k += 256) top = fmaxf(top, part.ml[(slot(k) * R + row) * 2]);
-    s_m[threadIdx.x] = top;
-    __syncthreads();
-    for (int o = 128; o; o >>= 1) {
-        if (threadIdx.x < o) s_m[threadIdx.x] = fmaxf(s_m[threadIdx.x], s_m[threadIdx.x + o]);
-        __syncthreads();
-    }
-    top = s_m[0];
-    const int grp = threadIdx.x / (DH / 4), c = 4 * (threadIdx.x % (DH / 4));
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
-#pragma unroll 4
-    for (int k = grp; k < count; k += G) {
-        const float2 ml = *reinterpret_cast<const float2 *>(part.ml + (slot(k) * R + row) * 2);
-        const float4 v = *reinterpret_cast<const float4 *>(part.o + (slot(k) * R + row) * DH + c);
-        if (ml.x == -INFINITY && ml.y == 0.0f) continue;
-        const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
-        sum = __fmaf_rn(ml.y, f, sum);
-        acc.x = __fmaf_rn(v.x, f, acc.x);
-        acc.y = __fmaf_rn(v.y, f, acc.y);
-        acc.z = __fmaf_rn(v.z, f, acc.z);
-        acc.w = __fmaf_rn(v.w, f, acc.w);
-    }
-    *reinterpret_cast<float4 *>(&s_o[grp][c]) = acc;
-    if (c == 0) s_l[grp] = sum;
-    __syncthreads();
-    if (grp == 0) {
-#pragma unroll
-        for (int k = 1; k < G; ++k) {
-            const float4 v = *reinterpret_cast<const float4 *>(&s_o[k][c]);
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
-        }
-        sum = 0.0f;
-#pragma unroll
-        for (int k = 0; k < G; ++k) sum += s_l[k];
-        store_row(p, s, me.qt * R + row, me.hk, c, DH, acc, top, sum);
-    }
-}
-
-// The same for units of many rows and few parts: 1024 / DH rows side by side.
-template <int DH>
-__global__ void __launch_bounds__(256) k_attention_kv8_join_rows(const AttnKV8Params p, int ctas, int R)
-{
-    wait_prior_grid();
-    const KV8Partials part(p.workspace, ctas, R, DH);
-    const int i = blockIdx.x + 1;
-    const KV8Meta me = part.meta[i];
-    if (me.j0 == 0) return;
-    const KV8Meta prev = part.meta[i - 1];
-    if (prev.j0 > 0 && prev.u0 == me.u0) return;
     const KV8Seq s = kv8_seq_checked(p.x, me.b);
     const int rows = min(R, s.n * p.ratio - me.qt * R);
-    int count = 2;
-    while (i - 1 + count < ctas) {
-        const KV8Meta c = part.meta[i - 1 + count];
-        if (c.j0 == 0 || c.u0 != me.u0) break;
-        ++count;
-    }
-    auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(i - 1) + (prev.u0 == me.u0 ? 0 : 1) : 2 * static_cast<int64_t>(i - 1 + k); };
-    constexpr int G = 256 / (DH / 4);
-    const int c = 4 * (threadIdx.x % (DH / 4));
-    for (int row = blockIdx.y * G + threadIdx.x / (DH / 4); row < rows; row += gridDim.y * G) {
+    const int64_t first = 2 * static_cast<int64_t>(i - 1) + (prev.u0 == me.u0 ? 0 : 1);
+    auto slot = [&](int k) { return k == 0 ? first : 2 * static_cast<int64_t>(i - 1 + k); };
+    for (int row = blockIdx.y * (8 / G) + warp / G; row < rows; row += gridDim.y * (8 / G)) {
         float top = -INFINITY;
-        for (int k = 0; k < count; ++k) top = fmaxf(top, part.ml[(slot(k) * R + row) * 2]);
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float sum = 0.0f;
-        for (int k = 0; k < count; ++k) {
+        for (int k = lane; k < count; k += 32) top = fmaxf(top, part.ml[(slot(k) * R + row) * 2]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+        float acc[CPL] = {}, sum = 0.0f;
+#pragma unroll 8
+        for (int k = warp % G; k < count; k += G) {
             const float2 ml = *reinterpret_cast<const float2 *>(part.ml + (slot(k) * R + row) * 2);
-            const float4 v = *reinterpret_cast<const float4 *>(part.o + (slot(k) * R + row) * DH + c);
-            if (ml.x == -INFINITY && ml.y == 0.0f) continue;
+            const float *src = part.o + (slot(k) * R + row) * DH + CPL * lane;
+            float v[CPL];
+            if (CPL == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(src);
+                v[0] = x.x;
+                v[1] = x.y;
+                v[CPL - 2] = x.z;
+                v[CPL - 1] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(src);
+                v[0] = x.x;
+                v[1] = x.y;
+            }
+            // a part that saw nothing has zeros
             const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
             sum = __fmaf_rn(ml.y, f, sum);
-            acc.x = __fmaf_rn(v.x, f, acc.x);
-            acc.y = __fmaf_rn(v.y, f, acc.y);
-            acc.z = __fmaf_rn(v.z, f, acc.z);
-            acc.w = __fmaf_rn(v.w, f, acc.w);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) acc[c] = __fmaf_rn(v[c], f, acc[c]);
         }
-        store_row(p, s, me.qt * R + row, me.hk, c, DH, acc, top, sum);
+        if (G > 1) {
+            __syncthreads();  // the row before's have been read
+            if (lane == 0) s_sum[warp] = sum;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) s_acc[warp][CPL * lane + c] = acc[c];
+            __syncthreads();
+            if (warp > 0) continue;
+            const int n = min(G, count);
+            for (int k = 1; k < n; ++k) {
+                sum += s_sum[k];
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) acc[c] += s_acc[k][CPL * lane + c];
+            }
+        }
+        store_row<CPL>(p, s, me.qt * R + row, me.hk, CPL * lane, DH, acc, top, sum);
     }
 }
 
@@ -511,14 +475,12 @@ cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t s
 
 cudaError_t attention_kv8_join_launch(const AttnKV8Params &p, int d_h, int ctas, int R, cudaStream_t stream)
 {
-    if (R <= 32) {
-        const dim3 grid(ctas - 1, R);
-        return d_h == 64 ? launch_after_prior(k_attention_kv8_join<64>, grid, dim3(256), 0, stream, p, ctas, R)
-                         : launch_after_prior(k_attention_kv8_join<128>, grid, dim3(256), 0, stream, p, ctas, R);
-    }
-    const dim3 grid(ctas - 1, 8);
-    return d_h == 64 ? launch_after_prior(k_attention_kv8_join_rows<64>, grid, dim3(256), 0, stream, p, ctas, R)
-                     : launch_after_prior(k_attention_kv8_join_rows<128>, grid, dim3(256), 0, stream, p, ctas, R);
+    const dim3 grid(ctas - 1, R > 32 ? 8 : R / 2);
+    if (R > 32)
+        return d_h == 64 ? launch_after_prior(k_attention_kv8_join<64, 1>, grid, dim3(256), 0, stream, p, ctas, R)
+                         : launch_after_prior(k_attention_kv8_join<128, 1>, grid, dim3(256), 0, stream, p, ctas, R);
+    return d_h == 64 ? launch_after_prior(k_attention_kv8_join<64, 8>, grid, dim3(256), 0, stream, p, ctas, R)
+                     : launch_after_prior(k_attention_kv8_join<128, 8>, grid, dim3(256), 0, stream, p, ctas, R);
 }
 
 size_t attention_kv8_workspace(int64_t T, int B, int Hq, int Hkv, int d_h)

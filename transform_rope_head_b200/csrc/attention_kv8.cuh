@@ -238,18 +238,24 @@ __device__ __forceinline__ int row_exponent(float amax)
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Four channels of row rr of (sequence s, key head hk): the normalised output (0 where the row saw
+// N channels of row rr of (sequence s, key head hk): the normalised output (0 where the row saw
 // nothing), and with the first ones the row's log-sum-exp.
+template <int N>
 __device__ __forceinline__ void store_row(const AttnKV8Params &p, const KV8Seq &s, int rr, int hk, int c, int d_h,
-                                          const float4 &acc, float top, float sum)
+                                          const float (&acc)[N], float top, float sum)
 {
-    const int64_t row = static_cast<int64_t>(s.q0 + rr / p.ratio) * p.Hq + hk * p.ratio + rr % p.ratio;
+    const int token = p.div_ratio(rr);
+    const int64_t row = static_cast<int64_t>(s.q0) * p.Hq + hk * p.ratio + rr + static_cast<int64_t>(token) * (p.Hq - p.ratio);
     const bool empty = top == -INFINITY && sum == 0.0f;
     const float inv = empty ? 0.0f : 1.0f / sum;
-    uint2 w;
-    w.x = empty ? 0u : pack16(acc.x * inv, acc.y * inv, p.half);
-    w.y = empty ? 0u : pack16(acc.z * inv, acc.w * inv, p.half);
-    *reinterpret_cast<uint2 *>(p.out + row * d_h + c) = w;
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = empty ? 0u : pack16(acc[2 * i] * inv, acc[2 * i + 1] * inv, p.half);
+    uint16_t *dst = p.out + row * d_h + c;
+    if (N == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[N / 2 - 1]);
+    else
+        *reinterpret_cast<uint32_t *>(dst) = w[0];
     if (c == 0 && p.lse) p.lse[row] = empty ? -INFINITY : (lg2(sum) + top) * 0.6931471805599453f;
 }
 

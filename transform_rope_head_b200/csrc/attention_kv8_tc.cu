@@ -32,10 +32,7 @@ constexpr int TC_THREADS = 16 * 32;
 constexpr int CONV0 = 8 * 32;      // first converting thread
 constexpr int MMA_WARP = 12;
 constexpr int QUERY_WARP = 14;
-#ifndef EXTRA_T
-#define EXTRA_T 3
-#endif
-constexpr int EXTRA = EXTRA_T;     // what a unit costs besides its tiles, in tiles
+constexpr int EXTRA = 3;           // what a unit costs besides its tiles, in tiles (1: 2 us more, 6: 5 us on 68)
 constexpr int RING = 4;            // tiles whose steps are kept
 constexpr int BLOCK = 128 * 128;   // bytes of 64 channels of 128 rows
 template <int DH>
@@ -592,11 +589,11 @@ __device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_half
                                              uint32_t o_cols, const RowMask &mask, RowState &r)
 {
     uint32_t a[32], b[32], pw[16];
-    tmem_ld32_async(s_cols, a);
-    tmem_ld32_async(s_cols + 32, b);
     float top = -INFINITY;
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
+        tmem_ld32_async(s_cols + 64 * h, a);
+        tmem_ld32_async(s_cols + 64 * h + 32, b);
         tmem_ld_wait(a);
         tmem_ld_wait(b);
         if (MASKED) {
@@ -604,9 +601,7 @@ __device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_half
             hide(b, mask.bits(64 * h + 32));
         }
         top = fmaxf(top, chunk_top(a, step + 4 * h));
-        if (h == 0) tmem_ld32_async(s_cols + 64, a);
         top = fmaxf(top, chunk_top(b, step + 4 * h + 2));
-        if (h == 0) tmem_ld32_async(s_cols + 96, b);
     }
     const bool moves = top > r.pass;
     if (__any_sync(FULL_MASK, moves)) {
@@ -631,23 +626,20 @@ __device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_half
             }
         }
     }
-    // backwards: the last two chunks are at hand, and P takes the upper columns once they are read
 #pragma unroll 1
     for (int h = 1; h >= 0; --h) {
+        tmem_ld32_async(s_cols + 64 * h, a);
+        tmem_ld32_async(s_cols + 64 * h + 32, b);
         const float4 c0 = step[4 * h], c1 = step[4 * h + 1], c2 = step[4 * h + 2], c3 = step[4 * h + 3];
-        if (h == 0) {
-            tmem_ld_wait(a);
-            tmem_ld_wait(b);
-            if (MASKED) {
-                hide(a, mask.bits(0));
-                hide(b, mask.bits(32));
-            }
+        tmem_ld_wait(a);
+        tmem_ld_wait(b);
+        if (MASKED) {
+            hide(a, mask.bits(64 * h));
+            hide(b, mask.bits(64 * h + 32));
         }
         chunk_p(b, c2, c3, r.m, pw, r.l);
-        if (h == 1) tmem_ld32_async(s_cols + 32, b);
         tmem_st16(s_cols + TS / 2 + 32 * h + 16, pw);
         chunk_p(a, c0, c1, r.m, pw, r.l);
-        if (h == 1) tmem_ld32_async(s_cols, a);
         tmem_st16(s_cols + TS / 2 + 32 * h, pw);
         tmem_st_wait();
         tc_fence_before();
