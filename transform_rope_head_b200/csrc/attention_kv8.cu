@@ -45,31 +45,69 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return r;
 }
 
-#ifndef EXTRA_S
-#define EXTRA_S 4
-#endif
-constexpr int EXTRA = EXTRA_S;  // what a unit costs besides its slices, in slices
+constexpr int EXTRA = 12;  // what a unit costs besides its slices, in slices
+constexpr int RING = 2;    // slices of a warp in use and on their way (3: as fast, 4: fewer warps fit)
+
+// A warp's slices on their way: codes by cp.async (what is in flight costs no registers), K rows then V rows.
+// 16-byte pieces of a row (of two rows of 64 channels) stand XORed among the 128 bytes' eight places so that
+// the fragments' reads meet no bank twice: K reads 4 neighbours of two rows at a time, V one piece
+// of every other row.
+template <int DH>
+struct __align__(128) Ring {
+    uint8_t codes[RING][2][16 * DH];
+    float ks[RING], vs[RING];
+    int page[RING];
+};
+
+template <int DH>
+__device__ __forceinline__ uint32_t piece(int row, int c)
+{
+    if (DH == 128) return row * 128 + ((c ^ (row & 6) ^ ((row & 1) << 2)) << 4);
+    return (row >> 1) * 128 + ((((row & 1) * 4 + c) ^ (((row >> 1) & 3) << 1)) << 4);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Starts the copies of the slice at tok0 (none without a page).
+template <int DH>
+__device__ __forceinline__ void start_slice(Ring<DH> &ring, int st, const AttnKV8Params &p, int page, int hk, int tok0, int lane)
+{
+    constexpr int PER_ROW = DH / 16, RPI = 32 / PER_ROW;
+    if (lane == 0) ring.page[st] = page;
+    const int64_t ph = static_cast<int64_t>(page < 0 ? 0 : page) * p.Hkv + hk;
+    const int64_t base = ((ph << p.x.page_shift) + (tok0 & ((1 << p.x.page_shift) - 1))) * DH + 16 * lane;
+    const int r = lane / PER_ROW, c = lane % PER_ROW;
+#pragma unroll
+    for (int i = 0; i < 16; i += RPI) {
+        copy16(smem_addr(ring.codes[st][0]) + piece<DH>(r + i, c), p.k_codes + base + i * DH);
+        copy16(smem_addr(ring.codes[st][1]) + piece<DH>(r + i, c), p.v_codes + base + i * DH);
+    }
+    if (lane == 0) copy4(smem_addr(&ring.ks[st]), p.k_steps + ph);
+    if (lane == 1) copy4(smem_addr(&ring.vs[st]), p.v_steps + ph);
+}
 
 // One slice's codes and steps as this lane holds them.
 template <int DH>
 struct Slice {
     uint32_t k[2][DH / 16];  // tokens g, g + 8: channels 16 t .. of each 64
     uint32_t v[4][DH / 32];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9: channels g * DH / 8 ..
-    float ks, vs;
 };
 
 template <int DH>
-__device__ __forceinline__ void load_slice(Slice<DH> &s, const AttnKV8Params &p, int page, int hk, int tok0, int g,
-                                           int t)
+__device__ __forceinline__ void read_slice(Slice<DH> &s, const Ring<DH> &ring, int st, int g, int t)
 {
-    const int pg = page < 0 ? 0 : page;
-    const int64_t ph = static_cast<int64_t>(pg) * p.Hkv + hk;
-    const int64_t base = ((ph << p.x.page_shift) + (tok0 & ((1 << p.x.page_shift) - 1))) * DH;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int c = 0; c < DH / 64; ++c) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p.k_codes + base + (g + 8 * r) * DH + 64 * c + 16 * t));
+            const uint4 w = *reinterpret_cast<const uint4 *>(ring.codes[st][0] + piece<DH>(g + 8 * r, 4 * c + t));
             s.k[r][4 * c] = w.x;
             s.k[r][4 * c + 1] = w.y;
             s.k[r][4 * c + 2] = w.z;
@@ -77,21 +115,19 @@ __device__ __forceinline__ void load_slice(Slice<DH> &s, const AttnKV8Params &p,
         }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const uint8_t *src = p.v_codes + base + (2 * t + (r & 1) + 8 * (r >> 1)) * DH + g * (DH / 8);
+        const int row = 2 * t + (r & 1) + 8 * (r >> 1);
         if (DH == 128) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(src));
+            const uint4 w = *reinterpret_cast<const uint4 *>(ring.codes[st][1] + piece<DH>(row, g));
             s.v[r][0] = w.x;
             s.v[r][1] = w.y;
             s.v[r][DH / 32 - 2] = w.z;
             s.v[r][DH / 32 - 1] = w.w;
         } else {
-            const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(src));
+            const uint2 w = *reinterpret_cast<const uint2 *>(ring.codes[st][1] + piece<DH>(row, g >> 1) + 8 * (g & 1));
             s.v[r][0] = w.x;
             s.v[r][1] = w.y;
         }
     }
-    s.ks = kv8_step(p.k_steps, ph);
-    s.vs = kv8_step(p.v_steps, ph);
 }
 
 template <int DH, int NT, int NW>
@@ -101,11 +137,13 @@ struct MergeSmem {
 };
 
 template <int DH, int NT, int NW>
-__global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p)
+__global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(const __grid_constant__ AttnKV8Params p)
 {
     constexpr int R = 8 * NT;     // query rows of a unit
     constexpr int KS = DH / 16;   // K-steps of S, M tiles of O
-    __shared__ __align__(16) MergeSmem<DH, NT, NW> sm;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Ring<DH> *const rings = reinterpret_cast<Ring<DH> *>(smem_raw);
+    MergeSmem<DH, NT, NW> &sm = *reinterpret_cast<MergeSmem<DH, NT, NW> *>(smem_raw + NW * sizeof(Ring<DH>));
     __shared__ KV8Start s_start;
     wait_prior_grid();
     allow_next_grid();
@@ -201,26 +239,45 @@ __global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p
             if (id < 0) flags |= ST_CACHE_INDEX;
             return id;
         };
-        Slice<DH> sl;
-        int j = j0 + warp;
-        int page = page_of(j);
-        if (j < j1) load_slice<DH>(sl, p, page, hk, token(j), g, t);
-        int page_next = page_of(j + NW);
+        Ring<DH> &ring = rings[warp];
+        int j = j0 + warp, st = 0;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < RING - 1; ++i) {
+            const int page = page_of(j + i * NW);
+            if (j + i * NW < j1) start_slice<DH>(ring, i, p, page, hk, token(j + i * NW), lane);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int page_next = page_of(j + (RING - 1) * NW);
         for (; j < j1; j += NW) {
+            // the copies RING - 1 slices on, into the place of the slice before
+            const int ahead = j + (RING - 1) * NW;
+            if (ahead < j1) start_slice<DH>(ring, st == 0 ? RING - 1 : st - 1, p, page_next, hk, token(ahead), lane);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            page_next = page_of(ahead + NW);
+            asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+            __syncwarp();
+            Slice<DH> sl;
+            read_slice<DH>(sl, ring, st, g, t);
+            const int page = ring.page[st];
+            const float ks = fminf(fmaxf(ring.ks[st], KV8_STEP_MIN), KV8_STEP_MAX);
+            const float vs = fminf(fmaxf(ring.vs[st], KV8_STEP_MIN), KV8_STEP_MAX);
+            st = st == RING - 1 ? 0 : st + 1;
             const int tok0 = token(j);
-            float sc[NT][4];
+            // two chains of sums, half as long
+            float sc[NT][4], sd[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[n][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) sc[n][e] = sd[n][e] = 0.0f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const uint32_t a0 = e4m3x2_to_half2(sl.k[0][k] & 0xffffu), a2 = e4m3x2_to_half2(sl.k[0][k] >> 16);
                 const uint32_t a1 = e4m3x2_to_half2(sl.k[1][k] & 0xffffu), a3 = e4m3x2_to_half2(sl.k[1][k] >> 16);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16(sc[n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
+                for (int n = 0; n < NT; ++n) mma_f16(k & 1 ? sd[n] : sc[n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
             }
-            const float ks = sl.ks, vs = sl.vs, lvs = lg2(vs), ivs = 1.0f / vs;
+            const float lvs = lg2(vs), ivs = 1.0f / vs;
             // every row sees every token of the slice?
             const bool full = page >= 0 && tok0 + 15 <= span.first &&
                               (p.window == 0 || tok0 > span.last - p.window || tok0 + 15 < p.sinks);
@@ -229,7 +286,7 @@ __global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    sc[n][e] = __fmaf_rn(sc[n][e], fac[n][e & 1] * ks, lvs);
+                    sc[n][e] = __fmaf_rn(sc[n][e] + sd[n][e], fac[n][e & 1] * ks, lvs);
                     if (!full) {
                         const int tok = tok0 + g + 8 * (e >> 1);
                         const int i = at[n][e & 1];
@@ -322,9 +379,7 @@ __global__ void __launch_bounds__(NW * 32) k_attention_kv8(const AttnKV8Params p
                         }
                     }
             }
-            page = page_next;
-            if (j + NW < j1) load_slice<DH>(sl, p, page, hk, token(j + NW), g, t);
-            page_next = page_of(j + 2 * NW);
+            __syncwarp();
         }
 
         // ---- join the warps ------------------------------------------------------------------
@@ -464,9 +519,12 @@ __global__ void __launch_bounds__(256) k_attention_kv8_join(const AttnKV8Params 
 template <int DH, int NT>
 cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t stream)
 {
-    constexpr int NW = 4;
-    const int ctas = dev.num_sms * 3 < KV8_MAX_CTAS ? dev.num_sms * 3 : KV8_MAX_CTAS;
-    const cudaError_t e = launch_after_prior(k_attention_kv8<DH, NT, NW>, dim3(ctas), dim3(NW * 32), 0, stream, p);
+    constexpr int NW = 4, PER_SM = NT == 1 ? 3 : 2;
+    constexpr int smem = NW * sizeof(Ring<DH>) + sizeof(MergeSmem<DH, NT, NW>);
+    const cudaError_t a = cudaFuncSetAttribute(k_attention_kv8<DH, NT, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (a != cudaSuccess) return a;
+    const int ctas = dev.num_sms * PER_SM < KV8_MAX_CTAS ? dev.num_sms * PER_SM : KV8_MAX_CTAS;
+    const cudaError_t e = launch_after_prior(k_attention_kv8<DH, NT, NW>, dim3(ctas), dim3(NW * 32), smem, stream, p);
     if (e != cudaSuccess) return e;
     return attention_kv8_join_launch(p, DH, ctas, 8 * NT, stream);
 }
@@ -475,7 +533,7 @@ cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t s
 
 cudaError_t attention_kv8_join_launch(const AttnKV8Params &p, int d_h, int ctas, int R, cudaStream_t stream)
 {
-    const dim3 grid(ctas - 1, R > 32 ? 8 : R / 2);
+    const dim3 grid(ctas - 1, R > 32 ? 16 : R / 2);
     if (R > 32)
         return d_h == 64 ? launch_after_prior(k_attention_kv8_join<64, 1>, grid, dim3(256), 0, stream, p, ctas, R)
                          : launch_after_prior(k_attention_kv8_join<128, 1>, grid, dim3(256), 0, stream, p, ctas, R);
@@ -487,18 +545,24 @@ size_t attention_kv8_workspace(int64_t T, int B, int Hq, int Hkv, int d_h)
 {
     if (T <= 0 || B <= 0) return 0;
     return kv8_takes_tc(T, B, Hq / Hkv) ? KV8Partials::bytes(KV8_TC_MAX_CTAS, KV8_TC_ROWS, d_h)
-                                        : KV8Partials::bytes(KV8_MAX_CTAS, 16, d_h);
+                                        : KV8Partials::bytes(KV8_MAX_CTAS, 24, d_h);
 }
 
 cudaError_t attention_kv8_launch(const AttnKV8Params &p, int d_h, const DeviceInfo &dev, cudaStream_t stream)
 {
     if (kv8_takes_tc(p.x.T, p.x.B, p.ratio)) return attention_kv8_tc_launch(p, d_h, dev, stream);
-    const bool two = p.x.cu != nullptr || p.ratio > 8;
+    // Query rows of a unit: what a sequence has.  The host does not know the counts; where they cannot all be
+    // alike it takes twice their mean, so that few sequences' caches are read twice (each 8 rows more take a
+    // third longer, a second unit twice as long).
+    const bool alike = !p.x.cu || p.x.T % p.x.B == 0;
+    const int64_t rows = (alike ? p.x.T / p.x.B : (2 * p.x.T + p.x.B - 1) / p.x.B) * p.ratio;
     cudaError_t e;
-    if (d_h == 64)
-        e = two ? launch<64, 2>(p, dev, stream) : launch<64, 1>(p, dev, stream);
+    if (rows <= 8)
+        e = d_h == 64 ? launch<64, 1>(p, dev, stream) : launch<128, 1>(p, dev, stream);
+    else if (rows <= 16)
+        e = d_h == 64 ? launch<64, 2>(p, dev, stream) : launch<128, 2>(p, dev, stream);
     else
-        e = two ? launch<128, 2>(p, dev, stream) : launch<128, 1>(p, dev, stream);
+        e = d_h == 64 ? launch<64, 3>(p, dev, stream) : launch<128, 3>(p, dev, stream);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
