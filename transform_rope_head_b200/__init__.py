@@ -439,41 +439,49 @@ def _kv8_dtype(t, name):
     raise ValueError(f"{name} must be bfloat16 or float16")
 
 
+# These two calls are made for every layer of every decoding step: the checks read each property once, and
+# pointers and streams go to the library as plain numbers.
+
 def _kv8_index(dev, T, cache, block_table, seq_lens, cu_new):
-    """Checks of the cache and the index tensors; (B, max_pages, num_pages, Hkv, page_size, d_h)."""
+    """Checks of the cache and the index tensors on CUDA device number ``dev``; (B, max_pages,
+    num_pages, Hkv, page_size, d_h)."""
     import torch
+    if dev < 0:
+        raise ValueError("tensors must be on a CUDA device")
     k, v, ks, vs = cache
-    num_pages, Hkv, ps, d_h = k.shape
-    if k.dtype is not torch.float8_e4m3fn or v.dtype is not torch.float8_e4m3fn:
+    shape, e4m3, f32, i32 = k.shape, torch.float8_e4m3fn, torch.float32, torch.int32
+    if k.dtype is not e4m3 or v.dtype is not e4m3:
         raise ValueError("cache codes must be float8_e4m3fn")
-    if ks.dtype is not torch.float32 or vs.dtype is not torch.float32:
+    if ks.dtype is not f32 or vs.dtype is not f32:
         raise ValueError("cache steps must be float32")
-    if v.shape != k.shape or tuple(ks.shape) != (num_pages, Hkv) or vs.shape != ks.shape:
+    if len(shape) != 4 or v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
         raise ValueError("cache shapes differ: codes [pages, Hkv, page_size, d_h], steps [pages, Hkv]")
-    if block_table.dim() != 2 or seq_lens.dim() != 1 or block_table.shape[0] != seq_lens.shape[0]:
+    table = block_table.shape
+    if len(table) != 2 or seq_lens.shape != table[:1]:
         raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-    B, max_pages = block_table.shape
-    index = [block_table, seq_lens]
-    if cu_new is not None:
-        if tuple(cu_new.shape) != (B + 1,):
+    B = table[0]
+    if cu_new is None:
+        if T != B:
+            raise ValueError("without cu_new there is one new token per sequence")
+        index = (block_table, seq_lens)
+    else:
+        if cu_new.shape != (B + 1,):
             raise ValueError("cu_new must be [B + 1]")
-        index.append(cu_new)
-    elif T != B:
-        raise ValueError("without cu_new there is one new token per sequence")
+        index = (block_table, seq_lens, cu_new)
     for t in index:
-        if t.dtype is not torch.int32:
+        if t.dtype is not i32:
             raise ValueError("block_table, seq_lens and cu_new must be int32")
     for t in (k, v, ks, vs, *index):
         if not t.is_contiguous():
             raise ValueError("the cache and the index tensors must be contiguous")
-        if t.device != dev:
+        if t.get_device() != dev:
             raise ValueError("all tensors must be on one CUDA device")
-    return B, max_pages, num_pages, Hkv, ps, d_h
+    return B, table[1], *shape
 
 
 def _kv8_rows(t, name, T, H, d_h, dtype, dev):
     """Elements from token to token of [T, H, d_h] rows (each token's heads contiguous)."""
-    if tuple(t.shape) != (T, H, d_h) or t.dtype is not dtype or t.device != dev:
+    if t.shape != (T, H, d_h) or t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name} must be [T, heads, d_h] of one type and device with the others")
     st, sh, sd = t.stride()
     if (sd != 1 or sh != d_h) and t.numel():
@@ -482,32 +490,32 @@ def _kv8_rows(t, name, T, H, d_h, dtype, dev):
     return st if T > 1 else max(st, H * d_h) // 8 * 8
 
 
-class _OnDevice:
-    """The tensors' device as the current one for a call (a no-op when it is), and its stream; new
-    tensors used on another stream than the allocating one are recorded on it."""
+def _kv8_stream(dev, stream, made):
+    """(the stream's handle, a guard or None): the tensors' device is made current where it is not, and
+    new tensors used on another stream than the allocating one are recorded on it."""
+    import torch
+    guard = torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
+    here = torch.cuda.current_stream(dev)
+    if stream is None:
+        return here.cuda_stream, guard
+    if stream != here:
+        for t in made:
+            t.record_stream(stream)
+    return stream.cuda_stream, guard
 
-    def __init__(self, dev, stream):
-        import torch
-        if dev.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        here = torch.cuda.current_stream(dev)
-        self.stream = here if stream is None else stream
-        self.other = self.stream if self.stream != here else None
-        self.guard = torch.cuda.device(dev) if torch.cuda.current_device() != dev.index else None
 
-    def new(self, t):
-        if self.other is not None:
-            t.record_stream(self.other)
-        return t
+def _kv8_call(fn, where, guard, *args):
+    if guard is None:
+        rc = fn(*args)
+    else:
+        with guard:
+            rc = fn(*args)
+    if rc != 0:
+        raise QKQError(rc, where)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def append_kv8(k, v, cache, block_table, seq_lens, cu_new=None, *, q=None, pos=None, cos_tab=None,
@@ -522,21 +530,21 @@ def append_kv8(k, v, cache, block_table, seq_lens, cu_new=None, *, q=None, pos=N
     channels (None: no rotation) at pos [T] int32 (None: each token's index in its sequence).
     k, v and q may be parts of one fused [T, heads, d_h] tensor.  Returns q_out (None without q)."""
     import torch
-    dev = k.device
-    T, _, d_h = k.shape
+    dev = k.get_device()
+    T, kt = k.shape[0], k.dtype
     dtype = _kv8_dtype(k, "k")
     B, max_pages, num_pages, Hkv, ps, dc = _kv8_index(dev, T, cache, block_table, seq_lens, cu_new)
-    ks = _kv8_rows(k, "k", T, Hkv, dc, k.dtype, dev)
-    vs = _kv8_rows(v, "v", T, Hkv, dc, k.dtype, dev)
-    on = _OnDevice(dev, stream)
-    Hq, qs = Hkv, 0
+    ks = _kv8_rows(k, "k", T, Hkv, dc, kt, dev)
+    vs = _kv8_rows(v, "v", T, Hkv, dc, kt, dev)
+    Hq, qs, made = Hkv, 0, ()
     if q is not None:
         Hq = q.shape[1]
-        qs = _kv8_rows(q, "q", T, Hq, dc, k.dtype, dev)
+        qs = _kv8_rows(q, "q", T, Hq, dc, kt, dev)
         if q_out is None:
-            q_out = on.new(torch.empty((T, Hq, dc), dtype=q.dtype, device=dev))
-        elif q_out.shape != q.shape or q_out.dtype is not q.dtype or not q_out.is_contiguous() \
-                or q_out.device != dev:
+            q_out = torch.empty((T, Hq, dc), dtype=kt, device=q.device)
+            made = (q_out,)
+        elif q_out.shape != q.shape or q_out.dtype is not kt or not q_out.is_contiguous() \
+                or q_out.get_device() != dev:
             raise ValueError("q_out must be a contiguous tensor like q")
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -544,21 +552,21 @@ def append_kv8(k, v, cache, block_table, seq_lens, cu_new=None, *, q=None, pos=N
     if (cos_tab is None) != (sin_tab is None):
         raise ValueError("cos_tab and sin_tab go together")
     if cos_tab is not None:
+        for t in (cos_tab, sin_tab):
+            if t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != dev \
+                    or t.dim() != 2 or t.shape != cos_tab.shape:
+                raise ValueError("cos_tab and sin_tab must be contiguous float32 [max_pos, rot_dim/2]")
         max_pos, rot = cos_tab.shape
         rot *= 2
-        for t in (cos_tab, sin_tab):
-            if t.dtype is not torch.float32 or not t.is_contiguous() or t.device != dev \
-                    or t.shape != cos_tab.shape:
-                raise ValueError("cos_tab and sin_tab must be contiguous float32 [max_pos, rot_dim/2]")
-    if pos is not None and (pos.dtype is not torch.int32 or tuple(pos.shape) != (T,)
-                            or not pos.is_contiguous() or pos.device != dev):
+    if pos is not None and (pos.dtype is not torch.int32 or pos.shape != (T,)
+                            or not pos.is_contiguous() or pos.get_device() != dev):
         raise ValueError("pos must be int32 [T]")
-    with on as s:
-        _check(_lib.qkq_append_kv8(
-            _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, dtype, _ptr(pos), T, _ptr(cu_new), _ptr(seq_lens),
-            B, _ptr(block_table), max_pages, num_pages, ps, Hq, Hkv, dc, rot, ROPE_STYLES[rope_style],
-            _ptr(cos_tab), _ptr(sin_tab), max_pos, _ptr(q_out), _ptr(cache.k), _ptr(cache.v),
-            _ptr(cache.k_steps), _ptr(cache.v_steps), _ptr(status), s), "qkq_append_kv8")
+    s, guard = _kv8_stream(dev, stream, made)
+    _kv8_call(_lib.qkq_append_kv8, "qkq_append_kv8", guard,
+              _addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, dtype, _addr(pos), T, _addr(cu_new),
+              seq_lens.data_ptr(), B, block_table.data_ptr(), max_pages, num_pages, ps, Hq, Hkv, dc, rot,
+              ROPE_STYLES[rope_style], _addr(cos_tab), _addr(sin_tab), max_pos, _addr(q_out),
+              cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), _addr(status), s)
     return q_out
 
 
@@ -574,34 +582,41 @@ def attention_kv8(q, cache, block_table, seq_lens, cu_new=None, *, scale=None, w
     cached tokens and the first ``sinks``.  scale: 1/sqrt(d_h) when None.  Returns out, or
     (out, lse) with want_lse or a given lse [T, Hq] fp32."""
     import torch
-    dev = q.device
-    T, Hq, d_h = q.shape
+    dev = q.get_device()
+    shape, qt = q.shape, q.dtype
+    T, Hq, d_h = shape
     dtype = _kv8_dtype(q, "q")
     B, max_pages, num_pages, Hkv, ps, dc = _kv8_index(dev, T, cache, block_table, seq_lens, cu_new)
     if dc != d_h or not q.is_contiguous():
         raise ValueError("q must be contiguous [T, Hq, d_h] with the cache's d_h")
-    on = _OnDevice(dev, stream)
+    made = []
     if out is None:
-        out = on.new(torch.empty_like(q))
-    elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous() or out.device != dev:
+        out = torch.empty_like(q)
+        made.append(out)
+    elif out.shape != shape or out.dtype is not qt or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous tensor like q")
-    if lse is None and want_lse:
-        lse = on.new(torch.empty((T, Hq), dtype=torch.float32, device=dev))
-    elif lse is not None and (tuple(lse.shape) != (T, Hq) or lse.dtype is not torch.float32
-                              or not lse.is_contiguous() or lse.device != dev):
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+            made.append(lse)
+    elif lse.shape != (T, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous() \
+            or lse.get_device() != dev:
         raise ValueError("lse must be contiguous float32 [T, Hq]")
     if workspace is None:
-        need = attention_kv8_workspace_bytes(T, B, Hq, Hkv, d_h)
-        workspace = on.new(torch.empty(need, dtype=torch.uint8, device=dev)) if need else None
-    elif workspace.device != dev or not workspace.is_contiguous():
+        size = _lib.qkq_attention_kv8_workspace_bytes(T, B, Hq, Hkv, d_h)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            made.append(workspace)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous on the tensors' device")
-    with on as s:
-        _check(_lib.qkq_attention_kv8(
-            _ptr(q), dtype, T, _ptr(cu_new), _ptr(seq_lens), B, _ptr(block_table), max_pages, num_pages,
-            ps, _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_steps), _ptr(cache.v_steps), Hq, Hkv, d_h,
-            float(d_h ** -0.5 if scale is None else scale), int(window), int(sinks), _ptr(out), _ptr(lse),
-            _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-            _ptr(status), s), "qkq_attention_kv8")
+    else:
+        size = workspace.numel() * workspace.element_size()
+    s, guard = _kv8_stream(dev, stream, made)
+    _kv8_call(_lib.qkq_attention_kv8, "qkq_attention_kv8", guard,
+              q.data_ptr(), dtype, T, _addr(cu_new), seq_lens.data_ptr(), B, block_table.data_ptr(), max_pages,
+              num_pages, ps, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
+              Hq, Hkv, d_h, float(d_h ** -0.5 if scale is None else scale), int(window), int(sinks), out.data_ptr(),
+              _addr(lse), _addr(workspace), size, _addr(status), s)
     return out if lse is None else (out, lse)
 
 

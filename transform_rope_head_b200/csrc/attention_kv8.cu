@@ -521,7 +521,8 @@ cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t s
 {
     constexpr int NW = 4, PER_SM = NT == 1 ? 3 : 2;
     constexpr int smem = NW * sizeof(Ring<DH>) + sizeof(MergeSmem<DH, NT, NW>);
-    const cudaError_t a = cudaFuncSetAttribute(k_attention_kv8<DH, NT, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t a = allow_smem(allowed, k_attention_kv8<DH, NT, NW>, smem, dev.ordinal);
     if (a != cudaSuccess) return a;
     const int ctas = dev.num_sms * PER_SM < KV8_MAX_CTAS ? dev.num_sms * PER_SM : KV8_MAX_CTAS;
     const cudaError_t e = launch_after_prior(k_attention_kv8<DH, NT, NW>, dim3(ctas), dim3(NW * 32), smem, stream, p);

@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 #include "kv8.cuh"
 
 namespace qkq {
@@ -264,6 +266,18 @@ __device__ __forceinline__ void store_row(const AttnKV8Params &p, const KV8Seq &
 // rows 110 us against 141, 32 rows 186 against 141; d_h 64: 86 against 129, 141 against 129).
 constexpr int KV8_TC_ROWS = 256, KV8_TC_MAX_CTAS = 160;
 inline bool kv8_takes_tc(int64_t T, int B, int ratio) { return T * ratio > static_cast<int64_t>(B) * 24; }
+// Allows a kernel its dynamic shared memory, once per device (the call costs more than a launch's arguments).
+// done: a bit per device ordinal, the kernel's own.
+template <typename Kernel>
+cudaError_t allow_smem(std::atomic<uint64_t> &done, Kernel kern, int bytes, int ordinal)
+{
+    const uint64_t bit = ordinal < 64 ? 1ull << ordinal : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 cudaError_t attention_kv8_tc_launch(const AttnKV8Params &p, int d_h, const DeviceInfo &dev, cudaStream_t stream);
 // Joins the partial rows that `ctas` CTAs left, R rows a unit.
 cudaError_t attention_kv8_join_launch(const AttnKV8Params &p, int d_h, int ctas, int R, cudaStream_t stream);

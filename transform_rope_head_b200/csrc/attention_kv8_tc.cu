@@ -836,7 +836,8 @@ template <int DH>
 cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t stream)
 {
     constexpr int smem = sizeof(TcSmem<DH>) + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(k_attention_kv8_tc<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(allowed, k_attention_kv8_tc<DH>, smem, dev.ordinal);
     if (e != cudaSuccess) return e;
     const int ctas = dev.num_sms < KV8_TC_MAX_CTAS ? dev.num_sms : KV8_TC_MAX_CTAS;
     const cudaError_t f = launch_after_prior(k_attention_kv8_tc<DH>, dim3(ctas), dim3(TC_THREADS), smem, stream, p);
