@@ -430,92 +430,33 @@ def kv8_cache(num_pages: int, Hkv: int, page_size: int, d_h: int, device="cuda")
     return KV8Cache(k, v, ks, vs)
 
 
-def _kv8_dtype(t, name):
-    import torch
-    if t.dtype is torch.bfloat16:
-        return 0
-    if t.dtype is torch.float16:
-        return 1
-    raise ValueError(f"{name} must be bfloat16 or float16")
+_native = None
 
 
-# These two calls are made for every layer of every decoding step: the checks read each property once, and
-# pointers and streams go to the library as plain numbers.
-
-def _kv8_index(dev, T, cache, block_table, seq_lens, cu_new):
-    """Checks of the cache and the index tensors on CUDA device number ``dev``; (B, max_pages,
-    num_pages, Hkv, page_size, d_h)."""
-    import torch
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    k, v, ks, vs = cache
-    shape, e4m3, f32, i32 = k.shape, torch.float8_e4m3fn, torch.float32, torch.int32
-    if k.dtype is not e4m3 or v.dtype is not e4m3:
-        raise ValueError("cache codes must be float8_e4m3fn")
-    if ks.dtype is not f32 or vs.dtype is not f32:
-        raise ValueError("cache steps must be float32")
-    if len(shape) != 4 or v.shape != shape or ks.shape != shape[:2] or vs.shape != shape[:2]:
-        raise ValueError("cache shapes differ: codes [pages, Hkv, page_size, d_h], steps [pages, Hkv]")
-    table = block_table.shape
-    if len(table) != 2 or seq_lens.shape != table[:1]:
-        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
-    B = table[0]
-    if cu_new is None:
-        if T != B:
-            raise ValueError("without cu_new there is one new token per sequence")
-        index = (block_table, seq_lens)
-    else:
-        if cu_new.shape != (B + 1,):
-            raise ValueError("cu_new must be [B + 1]")
-        index = (block_table, seq_lens, cu_new)
-    for t in index:
-        if t.dtype is not i32:
-            raise ValueError("block_table, seq_lens and cu_new must be int32")
-    for t in (k, v, ks, vs, *index):
-        if not t.is_contiguous():
-            raise ValueError("the cache and the index tensors must be contiguous")
-        if t.get_device() != dev:
-            raise ValueError("all tensors must be on one CUDA device")
-    return B, table[1], *shape
+def _binding():
+    """The compiled binding of the two calls that a decoding step makes for every layer (torch's
+    classes load with it, so it is imported at the first call)."""
+    global _native
+    if _native is None:
+        import importlib.util
+        import torch  # noqa: F401
+        path = os.path.join(_HERE, "_build", "qkq_binding.so")
+        if not os.path.exists(path):
+            raise ImportError(f"qkq_binding.so is not built ({path}); run "
+                              "`python transform_rope_head_b200/build.py`")
+        spec = importlib.util.spec_from_file_location("qkq_binding", path)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        mod.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            _lib.qkq_append_kv8, _lib.qkq_attention_kv8, _lib.qkq_attention_kv8_workspace_bytes)))
+        _native = mod
+    return _native
 
 
-def _kv8_rows(t, name, T, H, d_h, dtype, dev):
-    """Elements from token to token of [T, H, d_h] rows (each token's heads contiguous)."""
-    if t.shape != (T, H, d_h) or t.dtype is not dtype or t.get_device() != dev:
-        raise ValueError(f"{name} must be [T, heads, d_h] of one type and device with the others")
-    st, sh, sd = t.stride()
-    if (sd != 1 or sh != d_h) and t.numel():
-        if not (H == 1 and sd == 1):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st if T > 1 else max(st, H * d_h) // 8 * 8
-
-
-def _kv8_stream(dev, stream, made):
-    """(the stream's handle, a guard or None): the tensors' device is made current where it is not, and
-    new tensors used on another stream than the allocating one are recorded on it."""
-    import torch
-    guard = torch.cuda.device(dev) if torch.cuda.current_device() != dev else None
-    here = torch.cuda.current_stream(dev)
-    if stream is None:
-        return here.cuda_stream, guard
-    if stream != here:
-        for t in made:
-            t.record_stream(stream)
-    return stream.cuda_stream, guard
-
-
-def _kv8_call(fn, where, guard, *args):
-    if guard is None:
-        rc = fn(*args)
-    else:
-        with guard:
-            rc = fn(*args)
-    if rc != 0:
-        raise QKQError(rc, where)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _on_stream(t, stream):
+    """A new tensor that the call will use on ``stream``, which may not be the allocating one."""
+    t.record_stream(stream)
+    return t
 
 
 def append_kv8(k, v, cache, block_table, seq_lens, cu_new=None, *, q=None, pos=None, cos_tab=None,
@@ -529,44 +470,16 @@ def append_kv8(k, v, cache, block_table, seq_lens, cu_new=None, *, q=None, pos=N
     token per sequence).  cos_tab / sin_tab [max_pos, rot_dim/2] fp32 rotate the first rot_dim
     channels (None: no rotation) at pos [T] int32 (None: each token's index in its sequence).
     k, v and q may be parts of one fused [T, heads, d_h] tensor.  Returns q_out (None without q)."""
-    import torch
-    dev = k.get_device()
-    T, kt = k.shape[0], k.dtype
-    dtype = _kv8_dtype(k, "k")
-    B, max_pages, num_pages, Hkv, ps, dc = _kv8_index(dev, T, cache, block_table, seq_lens, cu_new)
-    ks = _kv8_rows(k, "k", T, Hkv, dc, kt, dev)
-    vs = _kv8_rows(v, "v", T, Hkv, dc, kt, dev)
-    Hq, qs, made = Hkv, 0, ()
-    if q is not None:
-        Hq = q.shape[1]
-        qs = _kv8_rows(q, "q", T, Hq, dc, kt, dev)
-        if q_out is None:
-            q_out = torch.empty((T, Hq, dc), dtype=kt, device=q.device)
-            made = (q_out,)
-        elif q_out.shape != q.shape or q_out.dtype is not kt or not q_out.is_contiguous() \
-                or q_out.get_device() != dev:
-            raise ValueError("q_out must be a contiguous tensor like q")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rot = max_pos = 0
-    if (cos_tab is None) != (sin_tab is None):
-        raise ValueError("cos_tab and sin_tab go together")
-    if cos_tab is not None:
-        for t in (cos_tab, sin_tab):
-            if t.dtype is not torch.float32 or not t.is_contiguous() or t.get_device() != dev \
-                    or t.dim() != 2 or t.shape != cos_tab.shape:
-                raise ValueError("cos_tab and sin_tab must be contiguous float32 [max_pos, rot_dim/2]")
-        max_pos, rot = cos_tab.shape
-        rot *= 2
-    if pos is not None and (pos.dtype is not torch.int32 or pos.shape != (T,)
-                            or not pos.is_contiguous() or pos.get_device() != dev):
-        raise ValueError("pos must be int32 [T]")
-    s, guard = _kv8_stream(dev, stream, made)
-    _kv8_call(_lib.qkq_append_kv8, "qkq_append_kv8", guard,
-              _addr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, dtype, _addr(pos), T, _addr(cu_new),
-              seq_lens.data_ptr(), B, block_table.data_ptr(), max_pages, num_pages, ps, Hq, Hkv, dc, rot,
-              ROPE_STYLES[rope_style], _addr(cos_tab), _addr(sin_tab), max_pos, _addr(q_out),
-              cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(), _addr(status), s)
+    handle = None
+    if stream is not None:
+        import torch
+        handle = stream.cuda_stream
+        if q is not None and q_out is None:
+            q_out = _on_stream(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+    rc, q_out = _binding().append(k, v, *cache, block_table, seq_lens, cu_new, q, pos, cos_tab, sin_tab,
+                                  ROPE_STYLES[rope_style], q_out, status, handle)
+    if rc:
+        raise QKQError(rc, "qkq_append_kv8")
     return q_out
 
 
@@ -581,42 +494,24 @@ def attention_kv8(q, cache, block_table, seq_lens, cu_new=None, *, scale=None, w
     written these tokens' keys and values.  window > 0 limits a token to its last ``window``
     cached tokens and the first ``sinks``.  scale: 1/sqrt(d_h) when None.  Returns out, or
     (out, lse) with want_lse or a given lse [T, Hq] fp32."""
-    import torch
-    dev = q.get_device()
-    shape, qt = q.shape, q.dtype
-    T, Hq, d_h = shape
-    dtype = _kv8_dtype(q, "q")
-    B, max_pages, num_pages, Hkv, ps, dc = _kv8_index(dev, T, cache, block_table, seq_lens, cu_new)
-    if dc != d_h or not q.is_contiguous():
-        raise ValueError("q must be contiguous [T, Hq, d_h] with the cache's d_h")
-    made = []
-    if out is None:
-        out = torch.empty_like(q)
-        made.append(out)
-    elif out.shape != shape or out.dtype is not qt or not out.is_contiguous() or out.get_device() != dev:
-        raise ValueError("out must be a contiguous tensor like q")
-    if lse is None:
-        if want_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-            made.append(lse)
-    elif lse.shape != (T, Hq) or lse.dtype is not torch.float32 or not lse.is_contiguous() \
-            or lse.get_device() != dev:
-        raise ValueError("lse must be contiguous float32 [T, Hq]")
-    if workspace is None:
-        size = _lib.qkq_attention_kv8_workspace_bytes(T, B, Hq, Hkv, d_h)
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-            made.append(workspace)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous on the tensors' device")
-    else:
-        size = workspace.numel() * workspace.element_size()
-    s, guard = _kv8_stream(dev, stream, made)
-    _kv8_call(_lib.qkq_attention_kv8, "qkq_attention_kv8", guard,
-              q.data_ptr(), dtype, T, _addr(cu_new), seq_lens.data_ptr(), B, block_table.data_ptr(), max_pages,
-              num_pages, ps, cache[0].data_ptr(), cache[1].data_ptr(), cache[2].data_ptr(), cache[3].data_ptr(),
-              Hq, Hkv, d_h, float(d_h ** -0.5 if scale is None else scale), int(window), int(sinks), out.data_ptr(),
-              _addr(lse), _addr(workspace), size, _addr(status), s)
+    handle = None
+    if want_lse and lse is None:
+        import torch
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        if stream is not None:
+            _on_stream(lse, stream)
+    if stream is not None:
+        import torch
+        handle = stream.cuda_stream
+        if out is None:
+            out = _on_stream(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+        if workspace is None:
+            need = attention_kv8_workspace_bytes(q.shape[0], seq_lens.shape[0], q.shape[1], cache[0].shape[1], q.shape[2])
+            workspace = _on_stream(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
+    rc, out = _binding().attention(q, *cache, block_table, seq_lens, cu_new, scale, window, sinks, out, lse, workspace,
+                                   status, handle)
+    if rc:
+        raise QKQError(rc, "qkq_attention_kv8")
     return out if lse is None else (out, lse)
 
 

@@ -22,6 +22,7 @@ OUT = os.environ.get("QKQ_BUILD_DIR") or os.path.join(HERE, "_build")
 OBJ = os.path.join(OUT, "obj")
 LIB = os.path.join(OUT, "libqkq.so")
 # the bounds-checking debug library (-DQKQ_BOUNDS_CHECK: index checks that set a status bit)
+BINDING = os.path.join(OUT, "qkq_binding.so")
 CHECK_OUT = os.path.join(HERE, "_build_check")
 CHECK_LIB = os.path.join(CHECK_OUT, "libqkq.so")
 
@@ -101,6 +102,32 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False,
     return lib_path
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile (if stale) csrc/binding.cpp against the installed torch; returns the module's path."""
+    import importlib.util
+    import sysconfig
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "qkq.h"), os.path.abspath(__file__)))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    os.makedirs(OUT, exist_ok=True)
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-I{os.path.join(ROOT, 'include')}", f"-I{sysconfig.get_paths()['include']}",
+           "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp, f"-L{os.path.join(torch, 'lib')}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding does not compile:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv,
                 ptxas_info="--ptxas" in sys.argv, check="--check" in sys.argv))
+    print(build_binding(force="--force" in sys.argv))
