@@ -167,6 +167,27 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
         const int j1 = static_cast<int>(min(static_cast<int64_t>(span.count), hi - u0 - EXTRA));
         const int rows = min(R, s.n * p.ratio - qt * R);
 
+        // ---- the warp's first slices, on their way while the queries come ---------------------
+        auto token = [&](int j) { return 16 * (j < span.head ? j : j + span.skip); };
+        auto page_of = [&](int j) {
+            const int tok = token(j);
+            if (j >= j1) return -1;
+            if (tok >= s.len) return -1;
+            const int id = kv8_page(x, b, tok >> x.page_shift);
+            if (id < 0) flags |= ST_CACHE_INDEX;
+            return id;
+        };
+        Ring<DH> &ring = rings[warp];
+        int j = j0 + warp, st = 0;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < RING - 1; ++i) {
+            const int page = page_of(j + i * NW);
+            if (j + i * NW < j1) start_slice<DH>(ring, i, p, page, hk, token(j + i * NW), lane);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        int page_next = page_of(j + (RING - 1) * NW);
+
         // ---- this unit's queries: B fragments, scaled per row into fp16 --------------------
         uint32_t qf[NT][KS][2];
         float fac[NT][2];   // rows 2t, 2t + 1 of each n-tile: scale log2(e) / the row's factor
@@ -230,25 +251,6 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
         }
 
         // ---- the warp's slices -------------------------------------------------------------
-        auto token = [&](int j) { return 16 * (j < span.head ? j : j + span.skip); };
-        auto page_of = [&](int j) {
-            const int tok = token(j);
-            if (j >= j1) return -1;
-            if (tok >= s.len) return -1;
-            const int id = kv8_page(x, b, tok >> x.page_shift);
-            if (id < 0) flags |= ST_CACHE_INDEX;
-            return id;
-        };
-        Ring<DH> &ring = rings[warp];
-        int j = j0 + warp, st = 0;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < RING - 1; ++i) {
-            const int page = page_of(j + i * NW);
-            if (j + i * NW < j1) start_slice<DH>(ring, i, p, page, hk, token(j + i * NW), lane);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
-        int page_next = page_of(j + (RING - 1) * NW);
         for (; j < j1; j += NW) {
             // the copies RING - 1 slices on, into the place of the slice before
             const int ahead = j + (RING - 1) * NW;

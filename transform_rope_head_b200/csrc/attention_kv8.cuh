@@ -64,8 +64,8 @@ __device__ __forceinline__ KV8Span unit_span(const AttnKV8Params &p, const KV8Se
 {
     KV8Span u;
     const int r0 = qt * R, r1 = min(r0 + R, s.n * p.ratio) - 1;
-    u.first = s.len - s.n + r0 / p.ratio;
-    u.last = s.len - s.n + r1 / p.ratio;
+    u.first = s.len - s.n + p.div_ratio(r0);
+    u.last = s.len - s.n + p.div_ratio(r1);
     const int end = max(u.last + 1, 0);  // <= len
     const int lo = p.window > 0 ? max(u.first - p.window + 1, 0) : 0;
     const int sink = p.window > 0 ? (min(p.sinks, end) + TS - 1) / TS : 0;
@@ -147,11 +147,11 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
 #pragma unroll
     for (int w = 0; w < NWARP; ++w) total += st.warp_sum[w];
     __syncthreads();
-    const int64_t most = (total + least - 1) / least;
-    const int64_t parts = most < static_cast<int64_t>(gridDim.x) ? most : gridDim.x;
-    const int64_t id = blockIdx.x;
-    const int64_t lo = id < parts ? total / parts * id + total % parts * id / parts : total;
-    const int64_t hi = id < parts ? total / parts * (id + 1) + total % parts * (id + 1) / parts : total;
+    // 64-bit divisions are long, and hardly a line needs them
+    const bool small = total < 0x7fffffff;
+    const int64_t share = small ? (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
+    const int64_t len = share < least ? least : share;
+    const int64_t lo = min(len * blockIdx.x, total), hi = min(lo + len, total);
     if (threadIdx.x == 0) {
         st.lo = lo;
         st.hi = hi;
@@ -206,10 +206,12 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
             }
             if (rem >= inc - w && rem < inc) {
                 const int64_t r = rem - (inc - w);
+                const int64_t h = small ? static_cast<uint32_t>(r) / static_cast<uint32_t>(c) : r / c;
+                const int at = static_cast<int>(r - h * c);
                 st.qt = q;
-                st.hk = static_cast<int>(r / c);
-                st.j0 = max(static_cast<int>(r % c) - extra, 0);
-                st.u0 = lo - r % c;
+                st.hk = static_cast<int>(h);
+                st.j0 = max(at - extra, 0);
+                st.u0 = lo - at;
             }
             const int64_t all = __shfl_sync(FULL_MASK, inc, 31);
             if (rem < all) break;

@@ -576,7 +576,7 @@ __device__ __forceinline__ void chunk_p(const uint32_t (&raw)[32], const float4 
     }
 }
 
-// A row's statistics: m the (whole-numbered) maximum's offset, l the sum, pass what a logit must
+// A row's statistics: m the maximum's offset, l the sum, pass what a logit must
 // exceed to move m (-inf: none seen yet).
 struct RowState {
     float m, l, pass;
@@ -605,9 +605,8 @@ __device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_half
     }
     const bool moves = top > r.pass;
     if (__any_sync(FULL_MASK, moves)) {
-        // the maximum moves: a whole number, so that every factor is a power of two (before a row's
-        // first logit there is nothing to rescale)
-        const float to = moves ? ceilf(top) : r.m;
+        // the maximum moves (before a row's first logit there is nothing to rescale)
+        const float to = moves ? top : r.m;
         const float alpha = !moves ? 1.0f : r.pass > -INFINITY ? ex2(r.m - to) : 0.0f;
         if (moves) {
             r.m = to;
