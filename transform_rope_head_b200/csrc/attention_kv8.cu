@@ -169,24 +169,40 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
 
         // ---- the warp's first slices, on their way while the queries come ---------------------
         auto token = [&](int j) { return 16 * (j < span.head ? j : j + span.skip); };
-        auto page_of = [&](int j) {
+        // pages as the table has them are checked when they are needed, not when they are asked for
+        auto raw_page = [&](int j) {
             const int tok = token(j);
-            if (j >= j1) return -1;
-            if (tok >= s.len) return -1;
-            const int id = kv8_page(x, b, tok >> x.page_shift);
-            if (id < 0) flags |= ST_CACHE_INDEX;
-            return id;
+            return j < j1 && tok < s.len ? __ldg(x.block_table + static_cast<int64_t>(b) * x.max_pages + (tok >> x.page_shift)) : -1;
+        };
+        auto checked = [&](int j, int raw) {
+            if (raw >= 0 && raw < x.num_pages) return raw;
+            if (j < j1 && token(j) < s.len) flags |= ST_CACHE_INDEX;
+            return -1;
         };
         Ring<DH> &ring = rings[warp];
         int j = j0 + warp, st = 0;
+        int raw[RING];
+#pragma unroll
+        for (int i = 0; i < RING; ++i) raw[i] = raw_page(j + i * NW);
+        uint4 qw[NT][DH / 32];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int rr = qt * R + 8 * n + g, tk = p.div_ratio(rr);
+            const uint16_t *src = p.q + (static_cast<int64_t>(s.q0 + tk) * p.Hq + hk * p.ratio + rr - tk * p.ratio) * DH + 16 * t;
+#pragma unroll
+            for (int c = 0; c < DH / 32; ++c) {
+                qw[n][c] = make_uint4(0, 0, 0, 0);
+                if (8 * n + g < rows) qw[n][c] = __ldg(reinterpret_cast<const uint4 *>(src + 64 * (c >> 1) + 8 * (c & 1)));
+            }
+        }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < RING - 1; ++i) {
-            const int page = page_of(j + i * NW);
-            if (j + i * NW < j1) start_slice<DH>(ring, i, p, page, hk, token(j + i * NW), lane);
+            const int ji = j + i * NW, page = checked(ji, raw[i]);
+            if (ji < j1) start_slice<DH>(ring, i, p, page, hk, token(ji), lane);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        int page_next = page_of(j + (RING - 1) * NW);
+        int raw_next = raw[RING - 1];
 
         // ---- this unit's queries: B fragments, scaled per row into fp16 --------------------
         uint32_t qf[NT][KS][2];
@@ -195,42 +211,29 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int row = 8 * n + g;
-            float f = 0.0f;
             float2 v[KS][2];
             float amax = 0.0f;
-            if (row < rows) {
-                const int rr = qt * R + row;
-                const uint16_t *src = p.q + (static_cast<int64_t>(s.q0 + rr / p.ratio) * p.Hq + hk * p.ratio + rr % p.ratio) * DH;
 #pragma unroll
-                for (int c = 0; c < DH / 64; ++c)
+            for (int c = 0; c < DH / 32; ++c) {
+                const uint32_t u[4] = {qw[n][c].x, qw[n][c].y, qw[n][c].z, qw[n][c].w};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 64 * c + 16 * t + 8 * h));
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[4 * c + 2 * h + (e >> 1)][e & 1] = unpack16(u[e], p.half);
-                    }
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        amax = fmaxf(amax, fabsf(v[k][e].x) <= 3.402823466e38f ? fabsf(v[k][e].x) : 0.0f);
-                        amax = fmaxf(amax, fabsf(v[k][e].y) <= 3.402823466e38f ? fabsf(v[k][e].y) : 0.0f);
-                    }
-            } else {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) v[k][0] = v[k][1] = make_float2(0.0f, 0.0f);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x2 = unpack16(u[e], p.half);
+                    v[2 * c + (e >> 1)][e & 1] = x2;
+                    amax = fmaxf(amax, fabsf(x2.x) <= 3.402823466e38f ? fabsf(x2.x) : 0.0f);
+                    amax = fmaxf(amax, fabsf(x2.y) <= 3.402823466e38f ? fabsf(x2.y) : 0.0f);
+                }
             }
             amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(FULL_MASK, amax, 2));
             const int e = row_exponent(amax);
             const float up = exp2i(-e);
-            f = p.scale_log2 * exp2i(e);
+            const float f = p.scale_log2 * exp2i(e);
 #pragma unroll
             for (int k = 0; k < KS; ++k)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) qf[n][k][h] = pack16(v[k][h].x * up, v[k][h].y * up, true);
-            const int idx = row < rows ? s.len - s.n + (qt * R + row) / p.ratio : -1;
+            const int idx = row < rows ? s.len - s.n + p.div_ratio(qt * R + row) : -1;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 fac[n][c] = __shfl_sync(FULL_MASK, f, (2 * t + c) * 4);
@@ -254,9 +257,10 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
         for (; j < j1; j += NW) {
             // the copies RING - 1 slices on, into the place of the slice before
             const int ahead = j + (RING - 1) * NW;
-            if (ahead < j1) start_slice<DH>(ring, st == 0 ? RING - 1 : st - 1, p, page_next, hk, token(ahead), lane);
+            const int page_ahead = checked(ahead, raw_next);
+            if (ahead < j1) start_slice<DH>(ring, st == 0 ? RING - 1 : st - 1, p, page_ahead, hk, token(ahead), lane);
             asm volatile("cp.async.commit_group;" ::: "memory");
-            page_next = page_of(ahead + NW);
+            raw_next = raw_page(ahead + NW);
             asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
             __syncwarp();
             Slice<DH> sl;
@@ -447,15 +451,15 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
 
 // Joins the partial rows of the units that a boundary between two CTAs cuts: boundary i does it for the unit
 // whose second part it opens.  G warps take a row (their lanes DH / 32 channels each, a warp every G-th part):
-// 8 where a unit of few rows may have a part on every SM, whose loads are then in flight together, 1 for
-// the many rows and few parts of the tensor-memory kernel.
+// 8 where few units of few rows have parts on many SMs, whose loads are then in flight together, 2 where many
+// units have few, 1 for the many rows and few parts of the tensor-memory kernel.
 template <int DH, int G>
-__global__ void __launch_bounds__(256) k_attention_kv8_join(const AttnKV8Params p, int ctas, int R)
+__global__ void __launch_bounds__(256, 5) k_attention_kv8_join(const AttnKV8Params p, int ctas, int R)
 {
     constexpr int CPL = DH / 32;
     __shared__ float s_sum[8], s_acc[8][DH];
+    // the next grid waits for this one to end: blocks of it that came earlier took a fifth longer for it all
     wait_prior_grid();
-    allow_next_grid();
     const KV8Partials part(p.workspace, ctas, R, DH);
     const int i = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const KV8Meta me = part.meta[i], prev = part.meta[i - 1];
@@ -472,7 +476,8 @@ __global__ void __launch_bounds__(256) k_attention_kv8_join(const AttnKV8Params 
     const int rows = min(R, s.n * p.ratio - me.qt * R);
     const int64_t first = 2 * static_cast<int64_t>(i - 1) + (prev.u0 == me.u0 ? 0 : 1);
     auto slot = [&](int k) { return k == 0 ? first : 2 * static_cast<int64_t>(i - 1 + k); };
-    for (int row = blockIdx.y * (8 / G) + warp / G; row < rows; row += gridDim.y * (8 / G)) {
+    for (int row0 = blockIdx.y * (8 / G); row0 < rows; row0 += gridDim.y * (8 / G)) {
+        const int row = min(row0 + warp / G, rows - 1);  // warps without a row do the last one too, and do not store it
         float top = -INFINITY;
         for (int k = lane; k < count; k += 32) top = fmaxf(top, part.ml[(slot(k) * R + row) * 2]);
 #pragma unroll
@@ -506,15 +511,15 @@ __global__ void __launch_bounds__(256) k_attention_kv8_join(const AttnKV8Params 
 #pragma unroll
             for (int c = 0; c < CPL; ++c) s_acc[warp][CPL * lane + c] = acc[c];
             __syncthreads();
-            if (warp > 0) continue;
+            if (warp % G > 0 || row0 + warp / G >= rows) continue;
             const int n = min(G, count);
             for (int k = 1; k < n; ++k) {
-                sum += s_sum[k];
+                sum += s_sum[warp + k];
 #pragma unroll
-                for (int c = 0; c < CPL; ++c) acc[c] += s_acc[k][CPL * lane + c];
+                for (int c = 0; c < CPL; ++c) acc[c] += s_acc[warp + k][CPL * lane + c];
             }
         }
-        store_row<CPL>(p, s, me.qt * R + row, me.hk, CPL * lane, DH, acc, top, sum);
+        if (row0 + warp / G < rows) store_row<CPL>(p, s, me.qt * R + row, me.hk, CPL * lane, DH, acc, top, sum);
     }
 }
 
@@ -536,12 +541,11 @@ cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t s
 
 cudaError_t attention_kv8_join_launch(const AttnKV8Params &p, int d_h, int ctas, int R, cudaStream_t stream)
 {
-    const dim3 grid(ctas - 1, R > 32 ? 16 : R / 2);
-    if (R > 32)
-        return d_h == 64 ? launch_after_prior(k_attention_kv8_join<64, 1>, grid, dim3(256), 0, stream, p, ctas, R)
-                         : launch_after_prior(k_attention_kv8_join<128, 1>, grid, dim3(256), 0, stream, p, ctas, R);
-    return d_h == 64 ? launch_after_prior(k_attention_kv8_join<64, 8>, grid, dim3(256), 0, stream, p, ctas, R)
-                     : launch_after_prior(k_attention_kv8_join<128, 8>, grid, dim3(256), 0, stream, p, ctas, R);
+    const auto launch_join = [&](auto kern, int y) { return launch_after_prior(kern, dim3(ctas - 1, y), dim3(256), 0, stream, p, ctas, R); };
+    if (R > 32) return d_h == 64 ? launch_join(k_attention_kv8_join<64, 1>, 16) : launch_join(k_attention_kv8_join<128, 1>, 16);
+    if (static_cast<int64_t>(p.x.B) * p.Hkv * 8 <= ctas)
+        return d_h == 64 ? launch_join(k_attention_kv8_join<64, 8>, R / 2) : launch_join(k_attention_kv8_join<128, 8>, R / 2);
+    return d_h == 64 ? launch_join(k_attention_kv8_join<64, 2>, R / 8) : launch_join(k_attention_kv8_join<128, 2>, R / 8);
 }
 
 size_t attention_kv8_workspace(int64_t T, int B, int Hq, int Hkv, int d_h)

@@ -88,20 +88,22 @@ __device__ __forceinline__ int unit_blocks(const AttnKV8Params &p, const KV8Seq 
     return (s.n * p.ratio + R - 1) / R;
 }
 
-// Tiles of a sequence over all its query blocks and key heads; each lane of the warp asks for its own
-// (b < 0: none).  Long lists of blocks are summed by the whole warp.
+// Places of a sequence on the line over all its query blocks and key heads; each lane of the warp asks for
+// its own (b < 0: none).  Long lists of blocks are summed by the whole warp.  one: the places of a unit
+// where the sequence has one query block, else 0.
 template <int TS>
-__device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, int b, int R, int extra, int lane)
+__device__ __forceinline__ int64_t seq_places(const AttnKV8Params &p, int b, int R, int extra, int lane, int &one, int &bad)
 {
     int64_t w = 0;
     int blocks = 0;
+    one = 0;
     if (b >= 0) {
+        bad |= !kv8_seq(p.x, b).ok;
         const KV8Seq s = kv8_seq_checked(p.x, b);
         blocks = unit_blocks(p, s, R);
-        if (blocks <= 2)
-            for (int q = 0; q < blocks; ++q) w += unit_span<TS>(p, s, q, R).count + extra;
+        if (blocks == 1) w = one = unit_span<TS>(p, s, 0, R).count + extra;
     }
-    for (unsigned m = __ballot_sync(FULL_MASK, blocks > 2); m; m &= m - 1) {
+    for (unsigned m = __ballot_sync(FULL_MASK, blocks > 1); m; m &= m - 1) {
         const int src = __ffs(m) - 1;
         const KV8Seq s = kv8_seq_checked(p.x, __shfl_sync(FULL_MASK, b, src));
         const int n = __shfl_sync(FULL_MASK, blocks, src);
@@ -117,8 +119,20 @@ __device__ __forceinline__ int64_t seq_tiles(const AttnKV8Params &p, int b, int 
 struct KV8Start {
     int64_t lo, hi, base, u0;
     int b, qt, hk, j0, flags;
-    int64_t warp_sum[32];
+    int found;  // qt, hk, j0 and u0 are in place
+    int64_t warp_sum[2][32];
 };
+
+// Place lo of a unit's c places per key head, r places after the first head's first.
+__device__ __forceinline__ void start_at(KV8Start &st, int64_t lo, int64_t r, int c, int extra, bool small)
+{
+    const int64_t h = small ? static_cast<uint32_t>(r) / static_cast<uint32_t>(c) : r / c;
+    const int at = static_cast<int>(r - h * c);
+    st.hk = static_cast<int>(h);
+    st.j0 = max(at - extra, 0);
+    st.u0 = lo - at;
+    st.found = 1;
+}
 
 // The CTA's part [lo, hi) of the line of all tiles (sequence, query block, key head, tile), on which a unit has
 // `extra` places before its tiles' (what beginning and ending it costs, in tiles), and the unit that holds lo:
@@ -131,22 +145,25 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int B = p.x.B;
     int64_t sum = 0, mine = 0;
-    int bad = 0;
+    int bad = 0, one = 0;
     for (int b0 = 0; b0 < B; b0 += THREADS) {
         const int b = b0 + static_cast<int>(threadIdx.x);
-        if (b < B) bad |= !kv8_seq(p.x, b).ok;
-        mine = seq_tiles<TS>(p, b < B ? b : -1, R, extra, lane);
+        mine = seq_places<TS>(p, b < B ? b : -1, R, extra, lane, one, bad);
         sum += mine;
     }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(FULL_MASK, sum, o);
+        if (lane >= o) sum += y;
+    }
+    if (lane == 31) st.warp_sum[0][warp] = sum;
     bad = __syncthreads_or(bad);
+    int64_t total = 0, before = 0;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
-    if (lane == 0) st.warp_sum[warp] = sum;
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < NWARP; ++w) total += st.warp_sum[w];
-    __syncthreads();
+    for (int w = 0; w < NWARP; ++w) {
+        if (w == warp) before = total;
+        total += st.warp_sum[0][w];
+    }
     // 64-bit divisions are long, and hardly a line needs them
     const bool small = total < 0x7fffffff;
     const int64_t share = small ? (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x : (total + gridDim.x - 1) / gridDim.x;
@@ -155,41 +172,57 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
     if (threadIdx.x == 0) {
         st.lo = lo;
         st.hi = hi;
-        st.b = st.qt = st.hk = st.j0 = 0;
         st.flags = bad ? ST_CACHE_INDEX : 0;
-        st.base = 0;
-        st.u0 = lo;
     }
     if (lo >= hi) {
+        if (threadIdx.x == 0) {
+            st.b = st.qt = st.hk = st.j0 = 0;
+            st.u0 = lo;
+        }
         __syncthreads();
         return;
     }
-    int64_t base = 0;
-    for (int b0 = 0; b0 < B; b0 += THREADS) {
-        const int b = b0 + static_cast<int>(threadIdx.x);
-        const int64_t w = B <= THREADS ? mine : seq_tiles<TS>(p, b < B ? b : -1, R, extra, lane);
-        int64_t inc = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(FULL_MASK, inc, o);
-            if (lane >= o) inc += y;
-        }
-        if (lane == 31) st.warp_sum[warp] = inc;
-        __syncthreads();
-        int64_t before = base;
-#pragma unroll
-        for (int k = 0; k < NWARP; ++k) {
-            if (k < warp) before += st.warp_sum[k];
-            base += st.warp_sum[k];
-        }
-        inc += before;
-        if (b < B && lo >= inc - w && lo < inc) {
-            st.b = b;
-            st.base = inc - w;
+    if (B <= THREADS) {
+        // a sequence a thread: the one that holds lo says where
+        sum += before;
+        if (lo >= sum - mine && lo < sum) {
+            st.b = threadIdx.x;
+            st.base = sum - mine;
+            st.qt = 0;
+            st.found = 0;
+            if (one) start_at(st, lo, lo - (sum - mine), one, extra, small);
         }
         __syncthreads();
-        if (lo < base) break;
+    } else {
+        int64_t base = 0;
+        if (threadIdx.x == 0) st.found = 0;
+        for (int b0 = 0; b0 < B; b0 += THREADS) {
+            const int b = b0 + static_cast<int>(threadIdx.x);
+            const int64_t w = seq_places<TS>(p, b < B ? b : -1, R, extra, lane, one, bad);
+            int64_t inc = w;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(FULL_MASK, inc, o);
+                if (lane >= o) inc += y;
+            }
+            if (lane == 31) st.warp_sum[1][warp] = inc;
+            __syncthreads();
+            int64_t first = base;
+#pragma unroll
+            for (int k = 0; k < NWARP; ++k) {
+                if (k < warp) first += st.warp_sum[1][k];
+                base += st.warp_sum[1][k];
+            }
+            inc += first;
+            if (b < B && lo >= inc - w && lo < inc) {
+                st.b = b;
+                st.base = inc - w;
+            }
+            __syncthreads();
+            if (lo < base) break;
+        }
     }
+    if (st.found) return;
     if (warp == 0) {
         const KV8Seq s = kv8_seq_checked(p.x, st.b);
         const int blocks = unit_blocks(p, s, R);
@@ -205,13 +238,8 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
                 if (lane >= o) inc += y;
             }
             if (rem >= inc - w && rem < inc) {
-                const int64_t r = rem - (inc - w);
-                const int64_t h = small ? static_cast<uint32_t>(r) / static_cast<uint32_t>(c) : r / c;
-                const int at = static_cast<int>(r - h * c);
                 st.qt = q;
-                st.hk = static_cast<int>(h);
-                st.j0 = max(at - extra, 0);
-                st.u0 = lo - at;
+                start_at(st, lo, rem - (inc - w), c, extra, small);
             }
             const int64_t all = __shfl_sync(FULL_MASK, inc, 31);
             if (rem < all) break;
