@@ -124,9 +124,11 @@ __device__ __forceinline__ float step_of(float amax)
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// DH channels; WPU warps (16 rows each) per page and head.
-template <int DH, int WPU>
-__global__ void __launch_bounds__(AK_WARPS * 32)
+// DH channels; WPU warps (16 rows each) per page and head.  BLOCKS on an SM: 3 for many tokens, where a few
+// spilled registers cost less than loads in flight gain (8 prompts of 4096: 153 us against 160), 2
+// for a token a sequence (256 sequences: 7.7 us against 7.9).
+template <int DH, int WPU, int BLOCKS>
+__global__ void __launch_bounds__(AK_WARPS * 32, BLOCKS)
 k_append_kv8(const AppendKV8Params p)
 {
     constexpr int NQ = DH / 16;        // lanes per row
@@ -320,15 +322,15 @@ k_append_kv8(const AppendKV8Params p)
     }
 }
 
-template <int DH>
+template <int DH, int BLOCKS>
 cudaError_t launch(const AppendKV8Params &p, int64_t ctas, cudaStream_t stream)
 {
     const dim3 grid(static_cast<unsigned>(ctas)), block(AK_WARPS * 32);
     switch (p.x.page_shift) {
-        case 4: return launch_after_prior(k_append_kv8<DH, 1>, grid, block, 0, stream, p);
-        case 5: return launch_after_prior(k_append_kv8<DH, 2>, grid, block, 0, stream, p);
-        case 6: return launch_after_prior(k_append_kv8<DH, 4>, grid, block, 0, stream, p);
-        default: return launch_after_prior(k_append_kv8<DH, 8>, grid, block, 0, stream, p);
+        case 4: return launch_after_prior(k_append_kv8<DH, 1, BLOCKS>, grid, block, 0, stream, p);
+        case 5: return launch_after_prior(k_append_kv8<DH, 2, BLOCKS>, grid, block, 0, stream, p);
+        case 6: return launch_after_prior(k_append_kv8<DH, 4, BLOCKS>, grid, block, 0, stream, p);
+        default: return launch_after_prior(k_append_kv8<DH, 8, BLOCKS>, grid, block, 0, stream, p);
     }
 }
 
@@ -344,7 +346,9 @@ cudaError_t append_kv8_launch(AppendKV8Params p, int d_h, cudaStream_t stream)
     const int64_t ctas = kv + (qw + AK_WARPS - 1) / AK_WARPS;
     if (ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
     p.kv_ctas = static_cast<unsigned>(kv);
-    const cudaError_t e = d_h == 64 ? launch<64>(p, ctas, stream) : launch<128>(p, ctas, stream);
+    const cudaError_t e = d_h == 64   ? launch<64, 2>(p, ctas, stream)
+                          : p.x.cu ? launch<128, 3>(p, ctas, stream)
+                                   : launch<128, 2>(p, ctas, stream);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
