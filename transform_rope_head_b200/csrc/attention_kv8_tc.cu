@@ -13,7 +13,9 @@
 // Warps: 0-3 and 4-7 one query tile each (a thread a row: no exchange for maxima or sums), 8-11
 // load and convert K and V two tiles ahead, 12 and 13 issue a query tile's MMAs each, S(i) | PV(i) S(i+1) | ...,
 // so that the tensor cores work on one query tile while the other's exponentials are taken, 14 and 15
-// fetch the next unit's queries.
+// fetch the next unit's queries.  A unit of at most 128 rows has one query tile; its tiles of tokens then go to
+// the two in turn, as two streams of their own that are joined at its end, so that the MMAs of one still
+// run beside the exponentials of the other.
 //
 // A row's thread reads S twice, for the maximum and for the exponentials, in chunks of 32 columns
 // and rolled loops: the roles together have to fit the instruction caches (fully unrolled, their
@@ -91,6 +93,10 @@ struct Units {
         j0 = 0;
         if (u0 + EXTRA < hi) next_unit(p, s, KV8_TC_ROWS, b, qt, hk);
     }
+    // A unit of one query tile: its token tiles go to the two query tiles' warps in turn.
+    __device__ __forceinline__ bool narrow() const { return rows <= 128; }
+    // Whether query tile t's warps have something of the unit.
+    __device__ __forceinline__ bool has(int t) const { return !narrow() || t < j1 - j0; }
     __device__ __forceinline__ int token(int j) const { return TS * (j < span.head ? j : j + span.skip); }
     __device__ __forceinline__ bool full(const AttnKV8Params &p, int tok0) const { return all_visible(p, span, tok0); }
 };
@@ -121,9 +127,10 @@ struct __align__(1024) TcSmem {
     // of the value step
     float4 step[RING][8];
     int2 tile[RING];                                // first token; whether every row sees all of the tile
+    float2 stats[2][128];                           // (maximum, sum) of a narrow unit's two streams
     int nan_unit[4];                                // number + 1 of the unit whose masked tiles hold NaN values
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t q_full[QBUF<DH>][2], q_empty[QBUF<DH>][2], s_full[2], p_half[2], p_full[2], o_done[2], drain;
+    uint64_t q_full[QBUF<DH>][2], q_empty[QBUF<DH>][2], s_full[2], p_half[2], p_full[2], o_done[2], streams[4], drain;
     uint32_t tmem;
     KV8Start start;
     Units units[TC_THREADS / 32];
@@ -378,7 +385,8 @@ __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> 
     return true;
 }
 
-// Query tile t of each unit, as it is, into the swizzled rows; rows that the unit has not become zero.
+// Query tile t of each unit (of a narrow one, the only one), as it is, into the swizzled rows; rows that the
+// unit has not become zero.
 template <int DH>
 __device__ __forceinline__ bool query_role(const AttnKV8Params &p, TcSmem<DH> &sm, int t)
 {
@@ -387,9 +395,9 @@ __device__ __forceinline__ bool query_role(const AttnKV8Params &p, TcSmem<DH> &s
     uint32_t phase = 0;  // bit buf: parity of that place's turn
     Units &u = sm.units[threadIdx.x >> 5];
     for (bool more = take_unit(p, sm.start, u, false); more; more = take_unit(p, sm.start, u, true)) {
-        const int buf = u.number % QBUF<DH>, rows = min(128, u.rows - t * 128);
-        if (rows <= 0) continue;
-        const int rr0 = u.qt * KV8_TC_ROWS + t * 128, token0 = p.div_ratio(rr0);
+        if (!u.has(t)) continue;
+        const int buf = u.number % QBUF<DH>, skip = u.narrow() ? 0 : t * 128, rows = min(128, u.rows - skip);
+        const int rr0 = u.qt * KV8_TC_ROWS + skip, token0 = p.div_ratio(rr0);
         const uint16_t *src = p.q + (static_cast<int64_t>(u.s.q0 + token0) * p.Hq + u.hk * p.ratio + rr0 - token0 * p.ratio) * DH + 8 * c8;
         const uint32_t dst = smem_addr(&sm.q[buf][t][0][0]);
         if (!warp_wait(smem_addr(&sm.q_empty[buf][t]), ((phase >> buf) & 1) ^ 1)) return false;
@@ -431,28 +439,23 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
     Units &u = sm.units[threadIdx.x >> 5];
     for (bool more = take_unit(p, sm.start, u, false); more; more = take_unit(p, sm.start, u, true)) {
         const int tiles = u.j1 - u.j0, buf = u.number % QBUF<DH>;
-        if (t * 128 >= u.rows) {
-            // nothing to do but to let the tiles go
-#pragma unroll 1
-            for (int j = 0; j < tiles; ++j, ++n) {
-                if (!warp_wait(smem_addr(&sm.k_full[n & 1]), (n >> 1) & 1)) return false;
-                if (elect_one()) mbar_arrive(smem_addr(&sm.k_empty[n & 1]));
-                if (!warp_wait(smem_addr(&sm.v_full[n & 1]), (n >> 1) & 1)) return false;
-                if (elect_one()) mbar_arrive(smem_addr(&sm.v_empty[n & 1]));
-                __syncwarp();
-            }
+        // its tiles: all, or of a narrow unit every other one, which nobody else reads
+        const bool narrow = u.narrow();
+        const int first = narrow ? t : 0, step = narrow ? 2 : 1, count = narrow ? (tiles + 1 - t) / 2 : tiles;
+        if (!u.has(t)) {
+            n += tiles;
             continue;
         }
         const uint64_t q = sw128_desc(smem_addr(&sm.q[buf][t][0][0]));
         if (!warp_wait(smem_addr(&sm.q_full[buf][t]), (q_phase >> buf) & 1)) return false;
         q_phase ^= 1u << buf;
 #pragma unroll 1
-        for (int j = 0; j <= tiles; ++j, ++n) {
-            const int st = n & 1;
-            if (j > 0) {
-                const uint64_t v = v0 + (st ^ 1) * STAGE;
-                const uint32_t add = j > 1 ? 1u : 0u;
-                if (!warp_wait(smem_addr(&sm.v_full[st ^ 1]), ((n - 1) >> 1) & 1)) return false;
+        for (int k = 0; k <= count; ++k) {
+            if (k > 0) {
+                const int i = n + first + (k - 1) * step, st = i & 1;
+                const uint64_t v = v0 + st * STAGE;
+                const uint32_t add = k > 1 ? 1u : 0u;
+                if (!warp_wait(smem_addr(&sm.v_full[st]), (i >> 1) & 1)) return false;
                 if (!warp_wait(smem_addr(&sm.p_half[t]), p_phase)) return false;
                 tc_fence_after();
                 if (elect_one()) {
@@ -467,30 +470,33 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
                 if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < TS / 32; ++s) mma_f16_ts(o_cols, s_cols + TS / 2 + 8 * s, v + s * (16 * 128 >> 4), id_o, 1u);
-                    mma_commit(smem_addr(&sm.v_empty[st ^ 1]));
-                    if (j == tiles) mma_commit(smem_addr(&sm.o_done[t]));
+                    mma_commit(smem_addr(&sm.v_empty[st]));
+                    if (narrow) mma_commit(smem_addr(&sm.v_empty[st]));
+                    if (k == count) mma_commit(smem_addr(&sm.o_done[t]));
                 }
                 __syncwarp();
             }
-            if (j < tiles) {
-                const uint64_t k = k0 + st * STAGE;
-                if (!warp_wait(smem_addr(&sm.k_full[st]), (n >> 1) & 1)) return false;
+            if (k < count) {
+                const int i = n + first + k * step, st = i & 1;
+                const uint64_t kd = k0 + st * STAGE;
+                if (!warp_wait(smem_addr(&sm.k_full[st]), (i >> 1) & 1)) return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < DH / 16; ++s) {
                         const uint32_t off = ((s >> 2) * BLOCK + (s & 3) * 32) >> 4;
-                        mma_bf16(s_cols, q + off, k + off, id_s, s ? 1u : 0u);
+                        mma_bf16(s_cols, q + off, kd + off, id_s, s ? 1u : 0u);
                     }
                     // done when all before it is, the last tile's values among that
                     mma_commit(smem_addr(&sm.s_full[t]));
                     mma_commit(smem_addr(&sm.k_empty[st]));
-                    if (j + 1 == tiles) mma_commit(smem_addr(&sm.q_empty[buf][t]));
+                    if (narrow) mma_commit(smem_addr(&sm.k_empty[st]));
+                    if (k + 1 == count) mma_commit(smem_addr(&sm.q_empty[buf][t]));
                 }
                 __syncwarp();
             }
         }
-        --n;
+        n += tiles;
     }
     return true;
 }
@@ -686,49 +692,91 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
     const int t = threadIdx.x >> 7, r = threadIdx.x & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(r & 96) << 16);
     const uint32_t s_cols = lanes + t * TS, o_cols = lanes + 2 * TS + t * DH;
-    int n = 0, cnt = 0, unit = 0;  // tiles of the part; tiles and units of this query tile
+    int n = 0, cnt = 0;        // tiles of the part, and of them this query tile's
+    uint32_t done[2] = {0, 0}; // parities of the query tiles' units
+    uint32_t met = 0;
+    // the two warps that have the same rows of the query tiles
+    auto meet = [&]() {
+        const uint32_t bar = smem_addr(&sm.streams[r >> 5]);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+        met ^= 1u;
+        return warp_wait(bar, met ^ 1u);
+    };
     Units &u = sm.units[threadIdx.x >> 5];
     for (bool more = take_unit(p, sm.start, u, false); more; more = take_unit(p, sm.start, u, true)) {
         const int tiles = u.j1 - u.j0;
-        if (t * 128 >= u.rows) {
+        const bool narrow = u.narrow(), two = narrow && tiles > 1;
+        const uint32_t done0 = done[0], done1 = done[1];
+        done[0] ^= 1u;
+        if (u.has(1)) {
+            done[1] ^= 1u;
+        } else if (!meet()) {  // the second tile's warps have ended what they had before the first's go on alone
+            return false;
+        }
+        if (!u.has(t)) {
             n += tiles;
             continue;
         }
-        const int row = t * 128 + r;
+        const int row = narrow ? r : t * 128 + r, step = narrow ? 2 : 1;
         const bool live = row < u.rows;
         const int at = live ? u.s.len - u.s.n + p.div_ratio(u.qt * KV8_TC_ROWS + row) : -1;
         RowState st{0.0f, 0.0f, -INFINITY};
+        const int last = n + tiles;
+        bool first = true;
 #pragma unroll 1
-        for (int j = 0; j < tiles; ++j, ++n, ++cnt) {
+        for (int i = narrow ? n + t : n; i < last; i += step, ++cnt) {
             if (!warp_wait(smem_addr(&sm.s_full[t]), cnt & 1)) return false;
             tc_fence_after();
-            const bool first = j == 0;
-            const int2 tile = sm.tile[n % RING];
+            const int2 tile = sm.tile[i % RING];
             const int hi = at - tile.x + 1;
             const RowMask mask{hi, p.window ? hi - p.window : 0, p.window ? p.sinks - tile.x : 0};
             const uint32_t p_half = smem_addr(&sm.p_half[t]), p_full = smem_addr(&sm.p_full[t]);
             if (tile.y)
-                softmax_tile<DH, false>(sm.step[n % RING], p_half, p_full, first, s_cols, o_cols, mask, st);
+                softmax_tile<DH, false>(sm.step[i % RING], p_half, p_full, first, s_cols, o_cols, mask, st);
             else
-                softmax_tile<DH, true>(sm.step[n % RING], p_half, p_full, first, s_cols, o_cols, mask, st);
+                softmax_tile<DH, true>(sm.step[i % RING], p_half, p_full, first, s_cols, o_cols, mask, st);
+            first = false;
         }
+        n = last;
 
         // ---- the unit's end ------------------------------------------------------------------------
-        if (!warp_wait(smem_addr(&sm.o_done[t]), unit & 1)) return false;
-        ++unit;
+        if (!warp_wait(smem_addr(&sm.o_done[t]), t ? done1 : done0)) return false;
+        float top = st.pass == -INFINITY ? -INFINITY : st.m, f0 = 1.0f, f1 = 0.0f;
+        if (two) {
+            // the other stream's sums stand in the same lanes: each of a row's two threads joins half of the channels
+            sm.stats[t][r] = make_float2(top, st.l);
+            if (!meet()) return false;
+            // complete by now (and its next turn is not): only the order of what was written is left to wait for
+            if (!warp_wait(smem_addr(&sm.o_done[t ^ 1]), t ? done0 : done1)) return false;
+            const float2 a = sm.stats[0][r], b = sm.stats[1][r];
+            top = fmaxf(a.x, b.x);
+            f0 = a.x == -INFINITY ? 0.0f : ex2(a.x - top);
+            f1 = b.x == -INFINITY ? 0.0f : ex2(b.x - top);
+            st.l = __fmaf_rn(b.y, f1, a.y * f0);
+        }
         tc_fence_after();
         const bool whole = u.j0 == 0 && u.j1 == u.span.count;
         const bool nan = *reinterpret_cast<volatile int *>(&sm.nan_unit[u.number & 3]) == u.number + 1;
-        const bool empty = st.pass == -INFINITY && st.l == 0.0f;
-        const float top = st.pass == -INFINITY ? -INFINITY : st.m;
+        const bool empty = top == -INFINITY && st.l == 0.0f;
         const int rr = u.qt * KV8_TC_ROWS + row, token = p.div_ratio(rr);
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u.number == 0 ? 0 : 1);
         const int64_t q_row = static_cast<int64_t>(u.s.q0) * p.Hq + u.hk * p.ratio + rr + static_cast<int64_t>(token) * (p.Hq - p.ratio);
         const float inv = empty ? 0.0f : 1.0f / st.l;
 #pragma unroll 1
-        for (int c = 0; c < DH; c += 16) {
+        for (int c = two ? t * (DH / 2) : 0; c < (two && t == 0 ? DH / 2 : DH); c += 16) {
             uint32_t raw[16];
-            tmem_ld16(o_cols + c, raw);
+            __syncwarp();
+            if (two) {
+                uint32_t other[16];
+                tmem_ld16(lanes + 2 * TS + c, raw);
+                tmem_ld16(lanes + 2 * TS + DH + c, other);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    raw[i] = __float_as_uint(__fmaf_rn(__uint_as_float(other[i]), f1, __uint_as_float(raw[i]) * f0));
+            } else {
+                tmem_ld16(o_cols + c, raw);
+            }
             if (!live) continue;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
@@ -753,13 +801,18 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
                 }
             }
         }
-        if (live) {
+        if (live && !(two && t == 1)) {
             if (!whole)
                 *reinterpret_cast<float2 *>(part.ml + (slot * KV8_TC_ROWS + row) * 2) = make_float2(top, st.l);
             else if (p.lse)
                 p.lse[q_row] = empty ? -INFINITY : (lg2(st.l) + top) * 0.6931471805599453f;
         }
         tc_fence_before();
+        if (two) {
+            // neither goes on to write O while the other reads it
+            if (!meet()) return false;
+            tc_fence_after();
+        }
     }
     return true;
 }
@@ -787,6 +840,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid
             mbar_init(smem_addr(&sm.p_half[i]), 4);
             mbar_init(smem_addr(&sm.p_full[i]), 4);
             mbar_init(smem_addr(&sm.o_done[i]), 1);
+            mbar_init(smem_addr(&sm.streams[2 * i]), 2);
+            mbar_init(smem_addr(&sm.streams[2 * i + 1]), 2);
         }
         mbar_init(smem_addr(&sm.drain), 2);
         fence_mbar_init();
