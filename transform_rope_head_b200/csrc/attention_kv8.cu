@@ -469,6 +469,7 @@ __global__ void __launch_bounds__(256, 5) k_attention_kv8_join(const AttnKV8Para
     const int i = blockIdx.x + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const KV8Meta me = part.meta[i], prev = part.meta[i - 1];
     if (me.j0 == 0 || (prev.j0 > 0 && prev.u0 == me.u0)) return;
+    const KV8Seq s = kv8_seq_checked(p.x, me.b);  // asked for before the parts are counted
     int count = 2;  // CTA i - 1, i, and those that go on with the unit
     for (bool on = true; on; ) {
         const int k = i - 1 + count + lane;
@@ -477,7 +478,6 @@ __global__ void __launch_bounds__(256, 5) k_attention_kv8_join(const AttnKV8Para
         count += n < 0 ? 32 : n;
         on = n < 0;
     }
-    const KV8Seq s = kv8_seq_checked(p.x, me.b);
     const int rows = min(R, s.n * p.ratio - me.qt * R);
     const int64_t first = 2 * static_cast<int64_t>(i - 1) + (prev.u0 == me.u0 ? 0 : 1);
     auto slot = [&](int k) { return k == 0 ? first : 2 * static_cast<int64_t>(i - 1 + k); };
