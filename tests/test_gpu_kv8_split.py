@@ -47,6 +47,15 @@ def test_prompt_rows_around_the_tiles(n, d, dtype):
     assert run_attention([n], [n % 5 * 40], 16, 4, 1, d, dtype, seed=n + d) == 0
 
 
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16")])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (140, 2)])
+def test_prompt_wide_and_narrow_units(d, dtype, window, sinks):
+    """Units of two query tiles and of one, whose token tiles go to two streams: one tile, two, odd counts, many."""
+    n = [70, 10, 33, 64, 31, 97, 8, 40, 32, 65]
+    cached = [0, 500, 95, 64, 1000, 160, 120, 0, 224, 300]
+    assert run_attention(n, cached, 32, 4, 1, d, dtype, window, sinks, seed=d + window) == 0
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (100, 0), (129, 5), (300, 200)])
 def test_prompt_windows(page, window, sinks):

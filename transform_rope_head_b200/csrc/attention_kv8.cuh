@@ -293,7 +293,7 @@ __device__ __forceinline__ void store_row(const AttnKV8Params &p, const KV8Seq &
 
 // Query rows a unit of the tensor-memory kernel has, and whether a call takes that kernel: from more than 24
 // rows a sequence on, what the register kernel takes in one unit (16 sequences of 8000 tokens, d_h 128: 24
-// rows 110 us against 141, 32 rows 186 against 141; d_h 64: 86 against 129, 141 against 129).
+// rows 101 us against 126, 32 rows 186 against 126; d_h 64: 73 against 101, 141 against 101).
 constexpr int KV8_TC_ROWS = 256, KV8_TC_MAX_CTAS = 160;
 inline bool kv8_takes_tc(int64_t T, int B, int ratio) { return T * ratio > static_cast<int64_t>(B) * 24; }
 // Allows a kernel its dynamic shared memory, once per device (the call costs more than a launch's arguments).
