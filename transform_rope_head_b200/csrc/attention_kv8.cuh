@@ -119,7 +119,7 @@ __device__ __forceinline__ int64_t seq_places(const AttnKV8Params &p, int b, int
 struct KV8Start {
     int64_t lo, hi, base, u0;
     int b, qt, hk, j0, flags;
-    int found;  // qt, hk, j0 and u0 are in place
+    int found;  // qt, hk, j0 and u0 are in place without the search by warp 0
     int64_t warp_sum[2][32];
 };
 
@@ -131,7 +131,6 @@ __device__ __forceinline__ void start_at(KV8Start &st, int64_t lo, int64_t r, in
     st.hk = static_cast<int>(h);
     st.j0 = max(at - extra, 0);
     st.u0 = lo - at;
-    st.found = 1;
 }
 
 // The CTA's part [lo, hi) of the line of all tiles (sequence, query block, key head, tile), on which a unit has
@@ -189,7 +188,7 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
             st.b = threadIdx.x;
             st.base = sum - mine;
             st.qt = 0;
-            st.found = 0;
+            st.found = one > 0;
             if (one) start_at(st, lo, lo - (sum - mine), one, extra, small);
         }
         __syncthreads();
@@ -222,6 +221,8 @@ __device__ __forceinline__ void find_start(const AttnKV8Params &p, KV8Start &st,
             if (lo < base) break;
         }
     }
+    // Written before the last barrier above and not again: every warp takes the same way here, however late
+    // it reads, and so the same barriers (the search below must not set it).
     if (st.found) return;
     if (warp == 0) {
         const KV8Seq s = kv8_seq_checked(p.x, st.b);
