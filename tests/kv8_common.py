@@ -143,16 +143,17 @@ def dev_reference(q, bt, scale, window=0, sinks=0):
     return [x.cpu().numpy() for x in (out, lse, mag, spread)]
 
 
-def check_dev(n, cached, page, Hq, Hkv, d, dtype="bf16", window=0, sinks=0, seed=0, cu_none=False, repeats=1):
+def check_dev(n, cached, page, Hq, Hkv, d, dtype="bf16", window=0, sinks=0, seed=0, cu_none=False, repeats=1,
+              loud=1.0):
     """attention_kv8 of a ``dev_batch`` against float64: every output within ``attention_bound``, the
-    log-sum-exps within theirs, status 0, and each repeat the same bits."""
+    log-sum-exps within theirs, status 0, and each repeat the same bits.  loud: the queries' spread."""
     import torch
     import transform_rope_head_b200 as qkq
     dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
     bt = dev_batch(n, cached, page, Hkv, d, seed)
     T = int(bt["host_cu"][-1])
     g = torch.Generator(device="cuda").manual_seed(int(seed) + 1)
-    q = torch.randn(T, Hq, d, generator=g, device="cuda").to(dt)
+    q = (torch.randn(T, Hq, d, generator=g, device="cuda") * loud).to(dt)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     args = (q, bt["cache"], bt["table"], bt["lens"], None if cu_none else bt["cu"])
     got = []
@@ -179,3 +180,27 @@ def lse_bound(lse, spread, L, d):
     roundings of a product acting on its spread); the result and its two summands (the offset, and the sum's
     logarithm with up to 40 for a value step and 20 for the count) are fp32 numbers."""
     return 2.0 ** -22 * (1 + L / 16 + 64) + 2.0 ** -22 * (np.abs(lse) + 60 + spread * (d + 3) / 2)
+
+
+def prompt_parts(n, cached, ratio, Hkv, ctas, window=0, sinks=0):
+    """The prompt kernel's work split on the host: per CTA the (query rows, token tiles) of its units.  A unit is
+    256 query rows of a sequence and key head, its places 3 and one per tile of 128 tokens that some
+    row sees; the line of all of them is cut in equal parts."""
+    units = []
+    for m, c in zip(n, cached):
+        for r0 in range(0, m * ratio, 256):
+            r1 = min(r0 + 256, m * ratio)
+            first, last = c + r0 // ratio, c + (r1 - 1) // ratio
+            seen = {j // 128 for j in range(last + 1) if not window or j > first - window or j < sinks}
+            units += [(r1 - r0, len(seen))] * Hkv
+    total = sum(t + 3 for _, t in units)
+    share = -(-total // ctas)
+    parts = [[] for _ in range(ctas)]
+    at = 0
+    for rows, tiles in units:
+        for i in range(at // share, (at + tiles + 2) // share + 1):
+            k = min(at + 3 + tiles, (i + 1) * share) - max(at + 3, i * share)
+            if k > 0:
+                parts[i].append((rows, k))
+        at += tiles + 3
+    return parts

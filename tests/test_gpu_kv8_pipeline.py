@@ -28,3 +28,85 @@ def test_drafted_tokens_in_several_units(window, sinks):
     n = r.integers(1, 9, 40)
     n[::5] = 12
     C.check_dev(n, r.integers(100, 3000, 40), 32, 8, 2, 128, "bf16", window, sinks, seed=4, repeats=4)
+
+
+# ---------------------------------------------------------------- the prompt kernel ------------
+
+def prompts(n, cached, Hkv, d, dtype, window=0, sinks=0, page=64, seed=0, loud=1.0, long=True):
+    """A batch for the prompt kernel (4 query heads a key head).  long: its line of tiles is long enough that
+    CTAs have several units, and in the mean 20 places."""
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    parts = C.prompt_parts(n, cached, 4, Hkv, ctas, window, sinks)
+    if long:
+        assert sum(3 + k for part in parts for _, k in part) >= 20 * ctas
+        assert max(len(part) for part in parts) > 1
+    C.check_dev(n, cached, page, 4 * Hkv, Hkv, d, dtype, window, sinks, seed=seed, repeats=3, loud=loud)
+    return parts
+
+
+def skips(part):
+    """Whether the second query tile's warps have nothing of some unit and go on to another of the part."""
+    return any(rows <= 128 and tiles == 1 for rows, tiles in part[:-1])
+
+
+HEADS = pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16"), (128, "fp16")])
+
+
+@HEADS
+def test_short_prompts_between_long_ones(d, dtype):
+    """Eight units of one query tile and one token tile in a row, wide units of many tiles around them."""
+    parts = prompts([3000, 20, 3000], [0, 30, 0], 8, d, dtype, seed=d)
+    assert any(skips(part) for part in parts)
+
+
+@HEADS
+def test_sixteen_prompts(d, dtype):
+    r = np.random.default_rng(d)
+    n = np.exp(r.uniform(np.log(16), np.log(2000), 16)).astype(int)
+    n[3], n[9] = 16, 2000
+    prompts(n, [0] * 16, 8, d, dtype, page=16, seed=d + 1)
+
+
+@HEADS
+@pytest.mark.parametrize("behind", [30, 100, 300])
+def test_decoding_tokens_beside_prompts(d, dtype, behind):
+    """Decoding tokens behind short caches in the same call as prompts of 2000 tokens, before, between and after them."""
+    n = [1] * 9 + [2000] + [1] * 12 + [2100] + [31] + [1] * 5
+    cached = [behind] * 9 + [0] + [behind + 7] * 12 + [500] + [300] + [behind] * 5
+    parts = prompts(n, cached, 8, d, dtype, page=32, seed=behind)
+    if behind < 128:
+        assert any(skips(part) for part in parts)
+
+
+@HEADS
+def test_odd_and_even_narrow_units_in_a_row(d, dtype):
+    """Units of one query tile with 7 and 9 token tiles, some with 8, 2 and 1: the streams change places."""
+    n = [32, 32, 20, 32, 7, 32, 32, 32] * 6
+    cached = [800, 1040, 850, 1100, 20, 1100, 900, 200] * 6
+    parts = prompts(n, cached, 8, d, dtype, seed=d + 2)
+    odd = sum(rows <= 128 and tiles % 2 == 1 and i + 1 < len(part) for part in parts for i, (rows, tiles) in enumerate(part))
+    assert odd > 20
+
+
+@HEADS
+def test_ragged_prompts_under_a_window(d, dtype):
+    prompts([1501, 700, 333, 1100, 40, 1400], [900, 0, 600, 300, 800, 20], 8, d, dtype, 1000, 3, page=16, seed=d + 3)
+
+
+@HEADS
+def test_rescaled_rows_of_many_tiles(d, dtype):
+    """Loud queries: a later tile's logits pass the running maximum, in wide units and in both streams of narrow ones."""
+    prompts([1100, 30, 1100, 32, 32, 25], [3000, 5000, 1000, 7000, 3000, 1000], 8, d, dtype, page=128, seed=d + 4, loud=12.0)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_drawn_batches(seed):
+    """Batches of every kind of unit, in any order."""
+    r = np.random.default_rng(seed)
+    B = int(r.integers(6, 40))
+    n = np.where(r.random(B) < 0.5, r.integers(1, 40, B), np.exp(r.uniform(np.log(2), np.log(1500), B)).astype(int))
+    n[r.integers(0, B)] = 1500
+    cached = np.where(r.random(B) < 0.3, 0, np.exp(r.uniform(0, np.log(4000), B)).astype(int))
+    window, sinks = [(0, 0), (int(r.integers(50, 1500)), int(r.integers(0, 200)))][seed % 2]
+    prompts(n, cached, int(r.choice([2, 8])), int(r.choice([64, 128])), str(r.choice(["bf16", "fp16"])), window, sinks,
+            page=int(r.choice([16, 32, 64, 128])), seed=seed, long=False)

@@ -423,7 +423,9 @@ __device__ __forceinline__ bool query_role(const AttnKV8Params &p, TcSmem<DH> &s
 }
 
 // The MMAs of query tile t, tile by tile: the tile before's values, then the tile's scores (which take the
-// columns that P leaves).
+// columns that P leaves).  Both MMA warps take part in every token tile, in order: what the other one computes (of a
+// narrow unit) a warp waits for and lets go.  A wait tells a barrier's phase from its neighbours only, so a warp
+// that passed over tiles could take an older phase for the one it means.
 template <int DH>
 __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm, uint32_t tmem, int t)
 {
@@ -436,19 +438,28 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
     const uint32_t s_cols = tmem + t * TS, o_cols = tmem + 2 * TS + t * DH;
     int n = 0;
     uint32_t q_phase = 0, p_phase = 0;  // parities: bit buf; bit 0
+    // tile i's keys or values, which the other warp reads
+    auto let_go = [&](uint64_t (&full)[2], uint64_t (&empty)[2], int i) {
+        if (!warp_wait(smem_addr(&full[i & 1]), (i >> 1) & 1)) return false;
+        if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&empty[i & 1]));
+        return true;
+    };
     Units &u = sm.units[threadIdx.x >> 5];
     for (bool more = take_unit(p, sm.start, u, false); more; more = take_unit(p, sm.start, u, true)) {
         const int tiles = u.j1 - u.j0, buf = u.number % QBUF<DH>;
-        // its tiles: all, or of a narrow unit every other one, which nobody else reads
+        // its tiles: all, or of a narrow unit every other one
         const bool narrow = u.narrow();
         const int first = narrow ? t : 0, step = narrow ? 2 : 1, count = narrow ? (tiles + 1 - t) / 2 : tiles;
         if (!u.has(t)) {
+            for (int i = n; i < n + tiles; ++i)
+                if (!let_go(sm.k_full, sm.k_empty, i) || !let_go(sm.v_full, sm.v_empty, i)) return false;
             n += tiles;
             continue;
         }
         const uint64_t q = sw128_desc(smem_addr(&sm.q[buf][t][0][0]));
         if (!warp_wait(smem_addr(&sm.q_full[buf][t]), (q_phase >> buf) & 1)) return false;
         q_phase ^= 1u << buf;
+        if (first > 0 && (!let_go(sm.k_full, sm.k_empty, n) || !let_go(sm.v_full, sm.v_empty, n))) return false;
 #pragma unroll 1
         for (int k = 0; k <= count; ++k) {
             if (k > 0) {
@@ -471,10 +482,10 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
 #pragma unroll
                     for (int s = 0; s < TS / 32; ++s) mma_f16_ts(o_cols, s_cols + TS / 2 + 8 * s, v + s * (16 * 128 >> 4), id_o, 1u);
                     mma_commit(smem_addr(&sm.v_empty[st]));
-                    if (narrow) mma_commit(smem_addr(&sm.v_empty[st]));
                     if (k == count) mma_commit(smem_addr(&sm.o_done[t]));
                 }
                 __syncwarp();
+                if (narrow && i + 1 < n + tiles && !let_go(sm.v_full, sm.v_empty, i + 1)) return false;
             }
             if (k < count) {
                 const int i = n + first + k * step, st = i & 1;
@@ -490,10 +501,11 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
                     // done when all before it is, the last tile's values among that
                     mma_commit(smem_addr(&sm.s_full[t]));
                     mma_commit(smem_addr(&sm.k_empty[st]));
-                    if (narrow) mma_commit(smem_addr(&sm.k_empty[st]));
                     if (k + 1 == count) mma_commit(smem_addr(&sm.q_empty[buf][t]));
                 }
                 __syncwarp();
+                // before this tile's softmax is waited for, so that the other stream's next keys can come
+                if (narrow && i + 1 < n + tiles && !let_go(sm.k_full, sm.k_empty, i + 1)) return false;
             }
         }
         n += tiles;
