@@ -453,9 +453,16 @@ def _binding():
     return _native
 
 
-def _on_stream(t, stream):
-    """A new tensor that the call will use on ``stream``, which may not be the allocating one."""
-    t.record_stream(stream)
+def _empty(shape, dtype, device, stream):
+    """A new tensor that a call on ``stream`` (None: the current one) writes.  It comes from that stream's memory,
+    which nothing queued on another stream still uses, and is not given away while the caller's
+    stream uses it."""
+    import torch
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -472,10 +479,9 @@ def append_kv8(k, v, cache, block_table, seq_lens, cu_new=None, *, q=None, pos=N
     k, v and q may be parts of one fused [T, heads, d_h] tensor.  Returns q_out (None without q)."""
     handle = None
     if stream is not None:
-        import torch
         handle = stream.cuda_stream
         if q is not None and q_out is None:
-            q_out = _on_stream(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+            q_out = _empty(q.shape, q.dtype, q.device, stream)
     rc, q_out = _binding().append(k, v, *cache, block_table, seq_lens, cu_new, q, pos, cos_tab, sin_tab,
                                   ROPE_STYLES[rope_style], q_out, status, handle)
     if rc:
@@ -497,17 +503,15 @@ def attention_kv8(q, cache, block_table, seq_lens, cu_new=None, *, scale=None, w
     handle = None
     if want_lse and lse is None:
         import torch
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        if stream is not None:
-            _on_stream(lse, stream)
+        lse = _empty(q.shape[:2], torch.float32, q.device, stream)
     if stream is not None:
         import torch
         handle = stream.cuda_stream
         if out is None:
-            out = _on_stream(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+            out = _empty(q.shape, q.dtype, q.device, stream)
         if workspace is None:
             need = attention_kv8_workspace_bytes(q.shape[0], seq_lens.shape[0], q.shape[1], cache[0].shape[1], q.shape[2])
-            workspace = _on_stream(torch.empty(need, dtype=torch.uint8, device=q.device), stream)
+            workspace = _empty((need,), torch.uint8, q.device, stream)
     rc, out = _binding().attention(q, *cache, block_table, seq_lens, cu_new, scale, window, sinks, out, lse, workspace,
                                    status, handle)
     if rc:
