@@ -19,8 +19,8 @@
 // Queries are scaled by a power of two per row into fp16's range (bf16's 8 bits fit its 11).  P is
 // rounded to fp16 (relative 2^-12 mean); sums, maxima and the output stay fp32.  The page's value step
 // goes into the exponent, w_j = p_j vs_j = 2^(s_j + log2 vs_j - m), so that m bounds what is
-// rounded, and the row sum takes w_j / vs_j.  The running maximum moves only when a logit passes it
-// by more than 2^8 (fp16 and fp32 hold that), which leaves most slices without any exchange.
+// rounded, and the row sum takes w_j / vs_j.  m moves only when a logit passes the largest one before by
+// more than 2^8 (KV8_SLACK), which leaves most slices without any exchange.
 //
 // Work split: the slices of all (sequence, query block, key head) in one line, each unit with 12 places
 // more for what beginning and ending it costs, cut into equal parts, one per CTA of a persistent grid,
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
                         const bool see = page >= 0 && tok <= i && (p.window == 0 || tok > i - p.window || tok < p.sinks);
                         if (!see) sc[n][e] = -INFINITY;
                     }
-                    passes |= sc[n][e] > m[n][e & 1] + 8.0f;
+                    passes |= sc[n][e] > m[n][e & 1] + (KV8_UP + KV8_SLACK);
                 }
             if (__any_sync(FULL_MASK, passes)) {
 #pragma unroll
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
                         float top = fmaxf(sc[n][c], sc[n][2 + c]);
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, off));
-                        top = fmaxf(top, m[n][c]);
+                        top = fmaxf(top - KV8_UP, m[n][c]);
                         const float alpha = m[n][c] == top ? 1.0f : ex2(m[n][c] - top);
                         m[n][c] = top;
                         l[n][c] *= alpha;
@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(NW * 32, NT == 1 ? 3 : 2) k_attention_kv8(cons
                 for (int e = 0; e < 4; ++e) w[e] = ex2(sc[n][e] - (m[n][e & 1] == -INFINITY ? 0.0f : m[n][e & 1]));
                 l[n][0] = __fmaf_rn(w[0] + w[2], ivs, l[n][0]);
                 l[n][1] = __fmaf_rn(w[1] + w[3], ivs, l[n][1]);
-                pb[n][0] = transpose8x8(pack16(w[0], w[1], true));
-                pb[n][1] = transpose8x8(pack16(w[2], w[3], true));
+                pb[n][0] = transpose8x8(pack_weights(w[0], w[1]));
+                pb[n][1] = transpose8x8(pack_weights(w[2], w[3]));
             }
             uint32_t bad[4][DH / 32];
             bool any_bad = false;

@@ -262,6 +262,22 @@ __device__ __forceinline__ void next_unit(const AttnKV8Params &p, const KV8Seq &
     } while (b < p.x.B - 1 && kv8_seq_checked(p.x, b).n == 0);
 }
 
+// The weights 2^(logit - m) are rounded to fp16 for their product with the values.  A row's m stands KV8_UP below
+// its largest logit when it moves, and moves when a logit passes that one by KV8_SLACK, so that rescaling is
+// rare: a weight is at most 2^(KV8_UP + KV8_SLACK) = 2^15, which fp16 holds, and what its subnormals
+// round off is 2^-(25 + KV8_UP) of the largest weight or less.  (With the largest logit itself as m, rows
+// that a first token of no value dominates by 2^25 were 7% off.)
+constexpr float KV8_SLACK = 8.0f, KV8_UP = 7.0f;
+
+// Two weights as fp16, to nearest.  Saturating: beyond logits of 2^24 the offset's own fp32 rounding can let a weight
+// pass 2^15, and an infinite one would make the row NaN.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // 2^e of a row's scaling into fp16: the row's largest magnitude goes to [2^14, 2^15), so that
 // what fp16 flushes is 2^-38 of it.
 __device__ __forceinline__ int row_exponent(float amax)

@@ -22,7 +22,8 @@
 // warps spent more time waiting for instructions than in any pipe).  A chunk is read and waited for in one
 // place: between a tensor-memory load and its wait the compiler may not move its registers.
 //
-// The maximum moves only when a logit passes it by more than 2^8, so rescaling what was summed is rare.
+// The weights' offset moves only when a logit passes the largest one before by more than 2^8 (KV8_SLACK), so rescaling
+// what was summed is rare.
 //
 // What bounds it: 4096 tokens behind 8192 (32 heads, d_h 128) take 818 us, 840 TFLOP/s or 0.51 of cuBLAS' rate.
 // Of a tile's 5000 cycles the tensor cores are busy 2050, the exponentials (16 a clock) 2050 and shared
@@ -594,7 +595,7 @@ __device__ __forceinline__ void chunk_p(const uint32_t (&raw)[32], const float4 
             x = ex2(x);
             y = ex2(y);
             sum = add_pair(sum, pair(x, y));
-            pw[8 * g + i] = pack16(x, y, true);
+            pw[8 * g + i] = pack_weights(x, y);
         }
         float x, y;
         unpair(sum, x, y);
@@ -602,7 +603,7 @@ __device__ __forceinline__ void chunk_p(const uint32_t (&raw)[32], const float4 
     }
 }
 
-// A row's statistics: m the maximum's offset, l the sum, pass what a logit must
+// A row's statistics: m the weights' offset, l the sum, pass what a logit must
 // exceed to move m (-inf: none seen yet).
 struct RowState {
     float m, l, pass;
@@ -632,11 +633,11 @@ __device__ __forceinline__ void softmax_tile(const float4 *step, uint32_t p_half
     const bool moves = top > r.pass;
     if (__any_sync(FULL_MASK, moves)) {
         // the maximum moves (before a row's first logit there is nothing to rescale)
-        const float to = moves ? top : r.m;
+        const float to = moves ? top - KV8_UP : r.m;
         const float alpha = !moves ? 1.0f : r.pass > -INFINITY ? ex2(r.m - to) : 0.0f;
         if (moves) {
             r.m = to;
-            r.pass = to + 8.0f;
+            r.pass = top + KV8_SLACK;
         }
         r.l *= alpha;
         if (!first) {
