@@ -439,8 +439,9 @@ size_t qkq_attention_kv8_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int 
  *   tokens that stay visible):
  *     out[t][h] = sum_j softmax_j(scale * q[t][h] . K[j][h / (Hq/Hkv)]) V[j][h / (Hq/Hkv)].
  *   A row that sees nothing (i < 0) gets zeros and a log-sum-exp of -inf.
- *   Products of the queries and the codes exact (queries of few rows scaled per row by a power of two
- *   into fp16, of many as they are), fp32 sums, softmax statistics and outputs in fp32, the output rounded
+ *   Queries times codes in exact products, but that queries of few rows (at most 24 a sequence in the mean) are
+ *   scaled per row by a power of two into fp16: exact for fp16 queries, and for bf16 ones down to 2^-31 of the
+ *   row's largest channel, smaller ones off by at most 2^-39 of that.  fp32 sums, softmax statistics and outputs in fp32, the output rounded
  *   once to dtype.  Probabilities, times their page's value step, are rounded to fp16 before their product with
  *   the codes: off by at most 2^-11 of themselves, or by 2^-32 of the row's largest where that is more.
  *   A cached NaN code reaches exactly the rows that see it; what lies in pages behind a sequence's length, or

@@ -10,6 +10,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import transform_rope_head_b200 as qkq  # noqa: E402
+from tests import kv8_common as C  # noqa: E402
 
 EPS = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 
@@ -114,3 +115,25 @@ def test_logits_beyond_fp32s_fractions(n, ratio, L, d, dtype, size, above):
     out, lse = qkq.attention_kv8(q, cache, table, lens, cu, scale=float(np.log(2.0)), want_lse=True)
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
     assert out.min() >= 0.5 / 1.01 and out.max() <= 2.0 * 1.01
+
+
+@pytest.mark.parametrize("below", [28, 31, 34])
+@pytest.mark.parametrize("n,ratio,L", [(1, 4, 700), (1, 24, 900), (40, 4, 900)])
+def test_one_loud_query_channel(n, ratio, L, below):
+    """A bf16 query channel 2^below over the others, where the keys are zero: the logits come from the others, which
+    are exact down to 2^-31 of the loud one and off by at most 2^-39 of it under that (in the few-rows kernel)."""
+    d = 128
+    bt = C.dev_batch([n], [L - n], 32, 1, d, below)
+    bt["cache"].k.view(torch.uint8)[..., 7] = 0
+    g = torch.Generator(device="cuda").manual_seed(below)
+    q = (torch.rand(n, ratio, d, generator=g, device="cuda") + 1.0) * torch.where(torch.rand(n, ratio, d, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    q[..., 7] = 2.0 ** below
+    q = q.bfloat16()
+    got = qkq.attention_kv8(q, bt["cache"], bt["table"], bt["lens"], bt["cu"])
+    ref, _, mag, spread = C.dev_reference(q, bt, d ** -0.5)
+    bound = C.attention_bound(ref, mag, spread, L, d, False)
+    if below > 31 and n * ratio <= 24:
+        # every other channel is at least 1: the logit is off by 2^(below - 39) of its spread, the weights in
+        # numerator and denominator by that
+        bound += mag * 2 * 2.0 ** (below - 39) * spread[..., None]
+    assert (np.abs(got.double().cpu().numpy() - ref) <= bound).all()
