@@ -454,7 +454,8 @@ size_t qkq_attention_kv8_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int 
  *     the softmax's denominator.
  *   workspace: at least qkq_attention_kv8_workspace_bytes(...) bytes, contents irrelevant; calls
  *     that may overlap on the GPU need one each.
- *   status: nullable, QKQ_STATUS_CACHE_INDEX (QKQ_STATUS_TIMEOUT: a bounded on-chip wait gave up).
+ *   status: nullable, QKQ_STATUS_CACHE_INDEX (QKQ_STATUS_TIMEOUT: a bounded on-chip wait gave up; the rows
+ *     that it concerns are NaN, with or without a status).
  * Returns QKQ_OK (T == 0 or B == 0: nothing), or a negative qkq_err (nothing launched).
  */
 int qkq_attention_kv8(const void *q, int dtype, int64_t T, const int32_t *cu_new,
@@ -617,6 +618,14 @@ int qkq_dequant_error_recompute(const void *k_bf16, const int32_t *pos, int64_t 
  * Returns QKQ_OK, QKQ_ERR_ARG (null status, limit 0 or above 100 ms), QKQ_ERR_ALIGN.
  */
 int qkq_selftest_bounded_wait(unsigned long long limit_ns, int *status, qkq_stream_t stream);
+
+/*
+ * qkq_selftest_attention_kv8_stall — test hook for the same path in qkq_attention_kv8's prompt kernel.
+ *   In this process's later launches of it the thread block `cta` (>= 0) waits for a tile that never comes, and
+ *   every on-chip wait gives up after limit_ns (at most 100 ms).  limit_ns 0: as usual again.
+ * Returns QKQ_OK or QKQ_ERR_ARG.
+ */
+int qkq_selftest_attention_kv8_stall(unsigned long long limit_ns, int cta);
 
 #ifdef __cplusplus
 }

@@ -45,6 +45,7 @@ SYMBOLS = ("qkq_version", "qkq_error_string", "qkq_status_string", "qkq_rope_tab
            "qkq_rope_table_split", "qkq_rope_table_rows",
            "qkq_transform_quantize", "qkq_transform_quantize_qkv", "qkq_transform_quantize_tc",
            "qkq_attention_scores", "qkq_attention_scores_tc", "qkq_attention_scores_mma", "qkq_transform_quantize_stats", "qkq_selftest_bounded_wait",
+           "qkq_selftest_attention_kv8_stall",
            "qkq_transform_quantize_calibrate",
            "qkq_moments_workspace_bytes", "qkq_accumulate_moments",
            "qkq_solve_angles", "qkq_dequant_error_workspace_bytes", "qkq_dequant_error",
@@ -91,6 +92,8 @@ def _load() -> ctypes.CDLL:
     L.qkq_transform_quantize_calibrate.restype = I
     L.qkq_selftest_bounded_wait.argtypes = [ctypes.c_ulonglong, P, P]
     L.qkq_selftest_bounded_wait.restype = I
+    L.qkq_selftest_attention_kv8_stall.argtypes = [ctypes.c_ulonglong, I]
+    L.qkq_selftest_attention_kv8_stall.restype = I
     L.qkq_attention_scores.argtypes = [P, I64, P, P, I64, I, I, I, I, P, P]
     L.qkq_attention_scores.restype = I
     L.qkq_attention_scores_tc.argtypes = [P, I64, P, P, I64, I, I, I, I, P, P, P]

@@ -706,6 +706,13 @@ int qkq_selftest_bounded_wait(unsigned long long limit_ns, int *status, qkq_stre
     return from_cuda(qkq::bounded_wait_selftest_launch(limit_ns, status, stream));
 }
 
+int qkq_selftest_attention_kv8_stall(unsigned long long limit_ns, int cta)
+{
+    if (limit_ns > 100000000ull || cta < 0) return QKQ_ERR_ARG;  // at most 100 ms
+    qkq::attention_kv8_stall(limit_ns, cta);
+    return QKQ_OK;
+}
+
 size_t qkq_moments_workspace_bytes(int64_t T, int Hq, int Hkv, int d_h)
 {
     return moments_ws(T, Hq, Hkv, d_h);

@@ -131,7 +131,7 @@ struct __align__(1024) TcSmem {
     float2 stats[2][128];                           // (maximum, sum) of a narrow unit's two streams
     int nan_unit[4];                                // number + 1 of the unit whose masked tiles hold NaN values
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-    uint64_t q_full[QBUF<DH>][2], q_empty[QBUF<DH>][2], s_full[2], p_half[2], p_full[2], o_done[2], streams[4], drain;
+    uint64_t q_full[QBUF<DH>][2], q_empty[QBUF<DH>][2], s_full[2], p_half[2], p_full[2], o_done[2], streams[4], drain, never;
     uint32_t tmem;
     KV8Start start;
     Units units[TC_THREADS / 32];
@@ -195,7 +195,7 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 
 // A bounded wait by whole warps: the lanes go on, or give up, together.  The warp sleeps in the wait (up to
 // 20 us a try): polling without the hint took a fifth of the kernel's issue slots.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns)
 {
     unsigned long long t0 = 0;
     for (;;) {
@@ -209,8 +209,12 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity)
         if (__any_sync(FULL_MASK, ok)) return true;
         const unsigned long long t = globaltimer_ns();
         if (t0 == 0) t0 = t;
-        if (__any_sync(FULL_MASK, t - t0 > WAIT_LIMIT_NS)) return false;
+        if (__any_sync(FULL_MASK, t - t0 > limit_ns)) return false;
     }
+}
+__device__ __forceinline__ bool warp_wait(const AttnKV8Params &p, uint32_t bar, uint32_t parity)
+{
+    return warp_wait(bar, parity, p.wait_limit_ns);
 }
 
 // Registers per thread of the warpgroups, 128 at launch: 2 x 136 + 144 + 96 = 4 x 128.
@@ -316,6 +320,7 @@ __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> 
         __syncwarp();
     };
 
+    if (static_cast<int>(blockIdx.x) == p.stalled_cta && !warp_wait(p, smem_addr(&sm.never), 0)) return false;
     u.begin(sm.start);
     bool more = u.open(p);
     int j = u.j0;
@@ -332,7 +337,7 @@ __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> 
         const int tok0 = u.token(j), end = u.s.len - tok0, number = u.number;
         const bool full = u.full(p, tok0);
         const uint32_t gone = none;
-        if (!warp_wait(smem_addr(&sm.k_empty[st]), par)) return false;
+        if (!warp_wait(p, smem_addr(&sm.k_empty[st]), par)) return false;
         if (lane < 2) {
             const bool here = !((gone >> lane) & 1);
             const float k1 = fminf(fmaxf(ks, KV8_STEP_MIN), KV8_STEP_MAX), v1 = fminf(fmaxf(vs, KV8_STEP_MIN), KV8_STEP_MAX);
@@ -377,7 +382,7 @@ __device__ __forceinline__ bool convert_role(const AttnKV8Params &p, TcSmem<DH> 
         } else if (gone) {
             clear(vw, gone, 128);
         }
-        if (!warp_wait(smem_addr(&sm.v_empty[st]), par)) return false;
+        if (!warp_wait(p, smem_addr(&sm.v_empty[st]), par)) return false;
         store(&sm.v[st][0][0], vw, 0u, false);
         if (lane == 0) mbar_arrive(smem_addr(&sm.v_full[st]));
         if (more) load(vw, v_at);
@@ -401,7 +406,7 @@ __device__ __forceinline__ bool query_role(const AttnKV8Params &p, TcSmem<DH> &s
         const int rr0 = u.qt * KV8_TC_ROWS + skip, token0 = p.div_ratio(rr0);
         const uint16_t *src = p.q + (static_cast<int64_t>(u.s.q0 + token0) * p.Hq + u.hk * p.ratio + rr0 - token0 * p.ratio) * DH + 8 * c8;
         const uint32_t dst = smem_addr(&sm.q[buf][t][0][0]);
-        if (!warp_wait(smem_addr(&sm.q_empty[buf][t]), ((phase >> buf) & 1) ^ 1)) return false;
+        if (!warp_wait(p, smem_addr(&sm.q_empty[buf][t]), ((phase >> buf) & 1) ^ 1)) return false;
         phase ^= 1u << buf;
 #pragma unroll 2
         for (int r8 = 0; r8 < 128; r8 += 8) {
@@ -441,7 +446,7 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
     uint32_t q_phase = 0, p_phase = 0;  // parities: bit buf; bit 0
     // tile i's keys or values, which the other warp reads
     auto let_go = [&](uint64_t (&full)[2], uint64_t (&empty)[2], int i) {
-        if (!warp_wait(smem_addr(&full[i & 1]), (i >> 1) & 1)) return false;
+        if (!warp_wait(p, smem_addr(&full[i & 1]), (i >> 1) & 1)) return false;
         if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&empty[i & 1]));
         return true;
     };
@@ -458,7 +463,7 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
             continue;
         }
         const uint64_t q = sw128_desc(smem_addr(&sm.q[buf][t][0][0]));
-        if (!warp_wait(smem_addr(&sm.q_full[buf][t]), (q_phase >> buf) & 1)) return false;
+        if (!warp_wait(p, smem_addr(&sm.q_full[buf][t]), (q_phase >> buf) & 1)) return false;
         q_phase ^= 1u << buf;
         if (first > 0 && (!let_go(sm.k_full, sm.k_empty, n) || !let_go(sm.v_full, sm.v_empty, n))) return false;
 #pragma unroll 1
@@ -467,8 +472,8 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
                 const int i = n + first + (k - 1) * step, st = i & 1;
                 const uint64_t v = v0 + st * STAGE;
                 const uint32_t add = k > 1 ? 1u : 0u;
-                if (!warp_wait(smem_addr(&sm.v_full[st]), (i >> 1) & 1)) return false;
-                if (!warp_wait(smem_addr(&sm.p_half[t]), p_phase)) return false;
+                if (!warp_wait(p, smem_addr(&sm.v_full[st]), (i >> 1) & 1)) return false;
+                if (!warp_wait(p, smem_addr(&sm.p_half[t]), p_phase)) return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -476,7 +481,7 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
                         mma_f16_ts(o_cols, s_cols + TS / 2 + 8 * s, v + s * (16 * 128 >> 4), id_o, s > TS / 32 ? 1u : add);
                 }
                 __syncwarp();
-                if (!warp_wait(smem_addr(&sm.p_full[t]), p_phase)) return false;
+                if (!warp_wait(p, smem_addr(&sm.p_full[t]), p_phase)) return false;
                 p_phase ^= 1u;
                 tc_fence_after();
                 if (elect_one()) {
@@ -491,7 +496,7 @@ __device__ __forceinline__ bool mma_role(const AttnKV8Params &p, TcSmem<DH> &sm,
             if (k < count) {
                 const int i = n + first + k * step, st = i & 1;
                 const uint64_t kd = k0 + st * STAGE;
-                if (!warp_wait(smem_addr(&sm.k_full[st]), (i >> 1) & 1)) return false;
+                if (!warp_wait(p, smem_addr(&sm.k_full[st]), (i >> 1) & 1)) return false;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -714,7 +719,7 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
         met ^= 1u;
-        return warp_wait(bar, met ^ 1u);
+        return warp_wait(p, bar, met ^ 1u);
     };
     Units &u = sm.units[threadIdx.x >> 5];
     for (bool more = take_unit(p, sm.start, u, false); more; more = take_unit(p, sm.start, u, true)) {
@@ -739,7 +744,7 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
         bool first = true;
 #pragma unroll 1
         for (int i = narrow ? n + t : n; i < last; i += step, ++cnt) {
-            if (!warp_wait(smem_addr(&sm.s_full[t]), cnt & 1)) return false;
+            if (!warp_wait(p, smem_addr(&sm.s_full[t]), cnt & 1)) return false;
             tc_fence_after();
             const int2 tile = sm.tile[i % RING];
             const int hi = at - tile.x + 1;
@@ -754,14 +759,14 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
         n = last;
 
         // ---- the unit's end ------------------------------------------------------------------------
-        if (!warp_wait(smem_addr(&sm.o_done[t]), t ? done1 : done0)) return false;
+        if (!warp_wait(p, smem_addr(&sm.o_done[t]), t ? done1 : done0)) return false;
         float top = st.pass == -INFINITY ? -INFINITY : st.m, f0 = 1.0f, f1 = 0.0f;
         if (two) {
             // the other stream's sums stand in the same lanes: each of a row's two threads joins half of the channels
             sm.stats[t][r] = make_float2(top, st.l);
             if (!meet()) return false;
             // complete by now (and its next turn is not): only the order of what was written is left to wait for
-            if (!warp_wait(smem_addr(&sm.o_done[t ^ 1]), t ? done0 : done1)) return false;
+            if (!warp_wait(p, smem_addr(&sm.o_done[t ^ 1]), t ? done0 : done1)) return false;
             const float2 a = sm.stats[0][r], b = sm.stats[1][r];
             top = fmaxf(a.x, b.x);
             f0 = a.x == -INFINITY ? 0.0f : ex2(a.x - top);
@@ -830,6 +835,31 @@ __device__ __forceinline__ bool softmax_role(const AttnKV8Params &p, TcSmem<DH> 
     return true;
 }
 
+// A wait of this CTA gave up: what its part was to give, its units' rows or their partial statistics, becomes NaN, so
+// that a caller who does not look at the status cannot take what stood there for results.  By the warps that have
+// kept the registers a called function may use.
+template <int DH>
+__device__ __noinline__ void void_part(const AttnKV8Params &p, const KV8Start &start)
+{
+    const KV8Partials part(p.workspace, gridDim.x, KV8_TC_ROWS, DH);
+    constexpr float NOT = __builtin_nanf("");
+    const uint32_t w = pack16(NOT, NOT, p.half);
+    Units u;
+    u.begin(start);
+    while (u.open(p)) {
+        const bool whole = u.j0 == 0 && u.j1 == u.span.count;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (u.number == 0 ? 0 : 1);
+        for (int i = threadIdx.x; i < u.rows * (DH / 8); i += MMA_WARP * 32) {
+            const int row = i / (DH / 8), c = i % (DH / 8), rr = u.qt * KV8_TC_ROWS + row;
+            const int64_t q_row = static_cast<int64_t>(u.s.q0) * p.Hq + u.hk * p.ratio + rr + static_cast<int64_t>(p.div_ratio(rr)) * (p.Hq - p.ratio);
+            if (whole) *reinterpret_cast<uint4 *>(p.out + q_row * DH + 8 * c) = make_uint4(w, w, w, w);
+            if (whole && c == 0 && p.lse) p.lse[q_row] = NOT;
+            if (!whole && c == 0) *reinterpret_cast<float2 *>(part.ml + (slot * KV8_TC_ROWS + row) * 2) = make_float2(0.0f, NOT);
+        }
+        u.close(p);
+    }
+}
+
 template <int DH>
 __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid_constant__ AttnKV8Params p)
 {
@@ -857,6 +887,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid
             mbar_init(smem_addr(&sm.streams[2 * i + 1]), 2);
         }
         mbar_init(smem_addr(&sm.drain), 2);
+        mbar_init(smem_addr(&sm.never), 1);  // nothing arrives
         fence_mbar_init();
 #pragma unroll
         for (int i = 0; i < 4; ++i) sm.nan_unit[i] = 0;
@@ -892,7 +923,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid
             // nothing of this CTA runs on when its tensor memory goes
             if (elect_one()) mma_commit(smem_addr(&sm.drain));
             __syncwarp();
-            ok &= warp_wait(smem_addr(&sm.drain), 0);
+            ok &= warp_wait(smem_addr(&sm.drain), 0, WAIT_LIMIT_NS);
         }
         __syncwarp();
     }
@@ -900,12 +931,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1) k_attention_kv8_tc(const __grid
     if (p.status && flags) atomicOr(p.status, flags);
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    const bool gave_up = __syncthreads_or(!ok);
     if (warp == MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (gave_up && warp < MMA_WARP) void_part<DH>(p, sm.start);
 }
+
+// The waits of a test: their limit, and the CTA whose first tile never comes.
+std::atomic<unsigned long long> wait_limit{WAIT_LIMIT_NS};
+std::atomic<int> stalled_cta{-1};
 
 template <int DH>
 cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t stream)
@@ -922,8 +958,17 @@ cudaError_t launch(const AttnKV8Params &p, const DeviceInfo &dev, cudaStream_t s
 
 }  // namespace
 
-cudaError_t attention_kv8_tc_launch(const AttnKV8Params &p, int d_h, const DeviceInfo &dev, cudaStream_t stream)
+void attention_kv8_stall(unsigned long long limit_ns, int cta)
 {
+    wait_limit.store(limit_ns ? limit_ns : WAIT_LIMIT_NS, std::memory_order_relaxed);
+    stalled_cta.store(limit_ns ? cta : -1, std::memory_order_relaxed);
+}
+
+cudaError_t attention_kv8_tc_launch(const AttnKV8Params &params, int d_h, const DeviceInfo &dev, cudaStream_t stream)
+{
+    AttnKV8Params p = params;
+    p.wait_limit_ns = wait_limit.load(std::memory_order_relaxed);
+    p.stalled_cta = stalled_cta.load(std::memory_order_relaxed);
     const cudaError_t e = d_h == 64 ? launch<64>(p, dev, stream) : launch<128>(p, dev, stream);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

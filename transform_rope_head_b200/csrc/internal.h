@@ -246,6 +246,8 @@ struct AttnKV8Params {
     float *lse;                 // [T][Hq], nullable
     void *workspace;
     int *status;                // nullable
+    unsigned long long wait_limit_ns;  // of a wait on the chip
+    int stalled_cta;            // tests: the CTA whose first tile never comes (-1: none)
 #ifdef __CUDACC__
     // n / ratio for 0 <= n < 2^31: the multiplier is off by less than 2^ratio_shift / ratio / 2^(31 + ratio_shift)
     __device__ __forceinline__ int div_ratio(int n) const
@@ -256,6 +258,9 @@ struct AttnKV8Params {
 };
 
 size_t attention_kv8_workspace(int64_t T, int B, int Hq, int Hkv, int d_h);
+// Test hook, for later launches of the prompt kernel in this process: the limit of the on-chip waits and the CTA
+// whose first tile never comes (limit 0: as usual).
+void attention_kv8_stall(unsigned long long limit_ns, int cta);
 cudaError_t attention_kv8_launch(const AttnKV8Params &p, int d_h, const DeviceInfo &dev,
                                  cudaStream_t stream);
 
