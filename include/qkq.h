@@ -447,6 +447,12 @@ size_t qkq_attention_kv8_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int 
  *   A cached NaN code reaches exactly the rows that see it; what lies in pages behind a sequence's length, or
  *   in masked places, reaches none.
  *   Deterministic for a device and the sizes and lengths.
+ *   One kernel serves a call, chosen by T * (Hq / Hkv) / B, the query rows of a sequence in the mean (up to 24, and
+ *   more), since the counts themselves are on the device.  A call that mixes single tokens with long pieces of prompts is
+ *   right but slow: sequences far from the mean read their cache more often, or leave most of a tile empty
+ *   (255 tokens behind up to 8000 and a piece of 1024 behind 4000, 32 heads over 8, d_h 128: 1166 us, as two
+ *   calls 343 + 129 us).  Order such a batch with the single tokens first and make two calls, each over its rows
+ *   of q and out, its sequences of block_table and seq_lens, and a cu_new of its own that begins at 0.
  * Arguments
  *   q [T][Hq][d_h] (device, dtype).  scale: finite (usually 1/sqrt(d_h)).  window >= 0 (0: none),
  *   sinks >= 0 (used with a window).

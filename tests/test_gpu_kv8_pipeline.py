@@ -11,6 +11,8 @@ torch = pytest.importorskip("torch")
 if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
+import transform_rope_head_b200 as qkq  # noqa: E402
+
 
 @pytest.mark.parametrize("B,most,Hq,Hkv,d,dtype", [(256, 6000, 8, 2, 128, "bf16"), (600, 3000, 4, 1, 64, "fp16"),
                                                    (129, 5000, 24, 1, 128, "bf16")])
@@ -110,3 +112,22 @@ def test_drawn_batches(seed):
     window, sinks = [(0, 0), (int(r.integers(50, 1500)), int(r.integers(0, 200)))][seed % 2]
     prompts(n, cached, int(r.choice([2, 8])), int(r.choice([64, 128])), str(r.choice(["bf16", "fp16"])), window, sinks,
             page=int(r.choice([16, 32, 64, 128])), seed=seed, long=False)
+
+
+@pytest.mark.parametrize("piece,behind", [(700, 0), (300, 2500), (1500, 1000)])
+def test_single_tokens_and_a_piece_in_one_call_and_in_two(piece, behind):
+    """255 decoding tokens and a piece of a prompt, which one kernel takes together (the few-rows one but for the
+    longest piece) and two kernels apart, as the documentation advises."""
+    B, Hq, Hkv, d = 255, 8, 2, 128
+    r = np.random.default_rng(piece)
+    n, cached = [1] * B + [piece], list(r.integers(1, 3000, B)) + [behind]
+    C.check_dev(n, cached, 32, Hq, Hkv, d, seed=piece, repeats=2)
+    bt = C.dev_batch(n, cached, 32, Hkv, d, piece)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(sum(n), Hq, d, generator=g, device="cuda").bfloat16()
+    ref, _, mag, spread = C.dev_reference(q, bt, d ** -0.5)
+    c, table, lens, cu = (bt[k] for k in ("cache", "table", "lens", "cu"))
+    out = torch.cat([qkq.attention_kv8(q[:B], c, table[:B], lens[:B]),
+                     qkq.attention_kv8(q[B:], c, table[B:], lens[B:], cu[B:] - B)])
+    bound = C.attention_bound(ref, mag, spread, int(bt["host_lens"].max()), d, False)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()

@@ -502,7 +502,11 @@ def attention_kv8(q, cache, block_table, seq_lens, cu_new=None, *, scale=None, w
     paged 8-bit ``cache`` (``qkq_attention_kv8``); index tensors as in append_kv8, which has
     written these tokens' keys and values.  window > 0 limits a token to its last ``window``
     cached tokens and the first ``sinks``.  scale: 1/sqrt(d_h) when None.  Returns out, or
-    (out, lse) with want_lse or a given lse [T, Hq] fp32."""
+    (out, lse) with want_lse or a given lse [T, Hq] fp32.
+
+    Single tokens and long pieces of prompts are faster in two calls than in one (the kernel is chosen by
+    the mean of their counts): with B1 single tokens first, ``q[:B1], block_table[:B1], seq_lens[:B1]`` and
+    ``q[B1:], block_table[B1:], seq_lens[B1:], cu_new[B1:] - B1``."""
     handle = None
     if want_lse and lse is None:
         import torch
