@@ -381,7 +381,10 @@ int qkq_attention_scores_mma(const void *q_bf16, int64_t Tq, const uint8_t *k_co
  *   The index tensors live on the device and are checked there: a page id outside
  *   [0, num_pages), a length above max_pages * page_size or a row range outside [0, T) sets
  *   QKQ_STATUS_CACHE_INDEX and that page or sequence is left out; nothing outside the buffers is
- *   read or written.
+ *   read or written.  So does qkq_append_kv8 with a length below the sequence's count of new tokens (a padded entry
+ *   of length 0 among them, unless cu_new gives it no rows); queries that then stand before the sequence's first
+ *   token are rotated as at position 0 (QKQ_STATUS_POS_RANGE).  qkq_attention_kv8 takes such a length: those
+ *   rows see nothing.
  *   Supported: d_h in {64, 128}, page_size in {16, 32, 64, 128}, max_pages * page_size <= 2^30,
  *   bf16 or fp16 tensors, any Hq that is a multiple of Hkv.  16-byte aligned q, k, v, q_out, out, codes, tables, workspace.
  */

@@ -137,3 +137,11 @@ def test_one_loud_query_channel(n, ratio, L, below):
         # numerator and denominator by that
         bound += mag * 2 * 2.0 ** (below - 39) * spread[..., None]
     assert (np.abs(got.double().cpu().numpy() - ref) <= bound).all()
+
+
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "fp16")])
+@pytest.mark.parametrize("n", [1, 40])
+def test_log_sum_exps_take_the_weights_unrounded(n, d, dtype):
+    """Short caches and small logits: the bound (152 x 2^-22 here) lies below what weights rounded to fp16 (2^-11 of
+    them, of two to five about as large) would add to their sum."""
+    C.check_dev([n] * 64, [1, 2, 3, 4] * 16 if n == 1 else [0] * 64, 16, 8, 2, d, dtype, seed=n, cu_none=n == 1, loud=0.05)
