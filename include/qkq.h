@@ -449,6 +449,7 @@ size_t qkq_attention_kv8_workspace_bytes(int64_t T, int B, int Hq, int Hkv, int 
  *   the codes: off by at most 2^-11 of themselves, or by 2^-32 of the row's largest where that is more.
  *   A cached NaN code reaches exactly the rows that see it; what lies in pages behind a sequence's length, or
  *   in masked places, reaches none.
+ *   Non-finite queries are not reported; a row whose logits are all -inf comes out as one that sees nothing.
  *   Deterministic for a device and the sizes and lengths.
  *   One kernel serves a call, chosen by T * (Hq / Hkv) / B, the query rows of a sequence in the mean (up to 24, and
  *   more), since the counts themselves are on the device.  A call that mixes single tokens with long pieces of prompts is

@@ -131,3 +131,46 @@ def test_single_tokens_and_a_piece_in_one_call_and_in_two(piece, behind):
                      qkq.attention_kv8(q[B:], c, table[B:], lens[B:], cu[B:] - B)])
     bound = C.attention_bound(ref, mag, spread, int(bt["host_lens"].max()), d, False)
     assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
+
+
+@HEADS
+@pytest.mark.parametrize("window,sinks", [(0, 0), (400, 3)])
+def test_nan_codes_in_batches_of_many_units(d, dtype, window, sinks):
+    """NaN codes scattered over values and a few keys, in tiles that all, some and no rows see: a NaN value makes one
+    channel of the rows that see it NaN, a NaN key whole rows, and nothing else changes."""
+    n, cached = [900, 20, 31, 1100, 5, 1, 1500], [300, 30, 1100, 0, 2000, 700, 10]
+    Hkv, ratio = 8, 4
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[dtype]
+    bt = C.dev_batch(n, cached, 32, Hkv, d, d)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    q = torch.randn(sum(n), Hkv * ratio, d, generator=g, device="cuda").to(dt)
+    bad = [torch.rand(bt["cache"].k.shape, generator=g, device="cuda") < r for r in (2e-7, 4e-6)]
+    clean = [torch.where(b, 0, c.view(torch.uint8)) for b, c in zip(bad, bt["cache"][:2])]
+    for b, c in zip(bad, bt["cache"][:2]):
+        c.view(torch.uint8)[b] = 0x7F
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        qkq.attention_kv8(q, bt["cache"], bt["table"], bt["lens"], bt["cu"], window=window, sinks=sinks, out=out, lse=lse, status=st)
+    assert st.item() == 0
+    ref, rl, mag, spread = C.dev_reference(q, dict(bt, cache=qkq.KV8Cache(*(c.view(torch.float8_e4m3fn) for c in clean), *bt["cache"][2:])),
+                                           d ** -0.5, window, sinks)
+    row_nan = torch.zeros(sum(n), Hkv, dtype=torch.bool, device="cuda")
+    val_nan = torch.zeros(sum(n), Hkv, d, dtype=torch.bool, device="cuda")
+    for b, L in enumerate(bt["host_lens"].tolist()):
+        q0, q1 = bt["host_cu"][b:b + 2].tolist()
+        ids = bt["table"][b, : -(-L // 32)].long()
+        kb, vb = (x[ids].transpose(0, 1).reshape(Hkv, -1, d)[:, :L] for x in bad)
+        i, j = L - (q1 - q0) + torch.arange(q1 - q0, device="cuda")[:, None], torch.arange(L, device="cuda")
+        see = (j <= i) & ((j > i - window) | (j < sinks) if window else j >= 0)
+        row_nan[q0:q1] = torch.einsum("tl,hl->th", see.float(), kb.any(-1).float()) > 0
+        val_nan[q0:q1] = torch.einsum("tl,hld->thd", see.float(), vb.float()) > 0
+    want = (val_nan | row_nan[..., None]).repeat_interleave(ratio, 1)
+    assert want.any() and not want.all()
+    assert torch.equal(torch.isnan(out), want)
+    assert torch.equal(torch.isnan(lse), row_nan.repeat_interleave(ratio, 1))
+    keep = ~want.cpu().numpy()
+    bound = C.attention_bound(ref, mag, spread, int(bt["host_lens"].max()), d, dtype == "fp16")
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound)[keep].all()
+    rows = ~torch.isnan(lse).cpu().numpy()
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= C.lse_bound(rl, spread, int(bt["host_lens"].max()), d))[rows].all()
