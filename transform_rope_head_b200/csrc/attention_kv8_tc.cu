@@ -25,11 +25,12 @@
 // The weights' offset moves only when a logit passes the largest one before by more than 2^8 (KV8_SLACK), so rescaling
 // what was summed is rare.
 //
-// What bounds it: 4096 tokens behind 8192 (32 heads, d_h 128) take 818 us, 840 TFLOP/s or 0.51 of cuBLAS' rate.
+// What bounds it: 4096 tokens behind 8192 (32 heads, d_h 128) take 817 to 841 us, 820 to 840
+// TFLOP/s or 0.5 of cuBLAS' rate.
 // Of a tile's 5000 cycles the tensor cores are busy 2050, the exponentials (16 a clock) 2050 and shared
 // memory 3000; the two query tiles' softmax overlaps each other's MMAs, but a tile's own chain of S, maximum,
 // P and PV is 3500 cycles long.  Tried: half rows on twice the warps 914 us (registers), 2^x of a quarter of
-// the columns by polynomial +4%, polling waits +4%.  2048 tokens, d_h 64: 68 us, where units of few tiles pay
+// the columns by polynomial +4%, polling waits +4%.  2048 tokens, d_h 64: 71 us, where units of few tiles pay
 // for their beginning and end.
 #include "attention_kv8.cuh"
 #include "tcgen05.cuh"
